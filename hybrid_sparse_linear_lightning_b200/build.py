@@ -7,17 +7,21 @@ import re
 import shutil
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libsala.so")
-SOURCES = ["api.cu"]
+SOURCES = ["api.cu", "packed.cu"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
-    "-O3", "-lineinfo", "-std=c++17", "-shared", "-Xcompiler", "-fPIC",
+    "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
     "--expt-relaxed-constexpr",
+]
+LINK_FLAGS = [
+    "-shared",
     # the decoder block's GEMMs
     "-lcublasLt", "-Xlinker", "-rpath,/usr/local/cuda/lib64",
 ]
@@ -75,22 +79,35 @@ def check_register_splits(regs: dict) -> None:
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     if not force and not needs_build():
         return LIB
-    cmd = [nvcc_path(), *NVCC_FLAGS, "-Xptxas", "-v", *extra, "-I", os.path.join(ROOT, "include"),
-           "-o", LIB + ".tmp", *[os.path.join(CSRC, s) for s in SOURCES]]
-    if verbose:
-        print(" ".join(cmd), file=sys.stderr)
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        sys.stderr.write(r.stdout + r.stderr)
-        raise subprocess.CalledProcessError(r.returncode, cmd)
+    obj_dir = os.path.join(PKG, "_build")
+    os.makedirs(obj_dir, exist_ok=True)
+    objs = [os.path.join(obj_dir, s + ".o") for s in SOURCES]
+
+    def run(cmd):
+        if verbose:
+            print(" ".join(cmd), file=sys.stderr)
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            sys.stderr.write(r.stdout + r.stderr)
+            raise subprocess.CalledProcessError(r.returncode, cmd)
+        return r.stdout + r.stderr
+
+    def compile_one(src_obj):
+        src, obj = src_obj
+        return run([nvcc_path(), *NVCC_FLAGS, "-Xptxas", "-v", *extra, "-I",
+                    os.path.join(ROOT, "include"), "-c", "-o", obj, os.path.join(CSRC, src)])
+
+    with ThreadPoolExecutor(len(SOURCES)) as pool:   # one nvcc per source, side by side
+        text = "".join(pool.map(compile_one, zip(SOURCES, objs)))
+    run([nvcc_path(), *NVCC_FLAGS, *LINK_FLAGS, "-o", LIB + ".tmp", *objs])
     cur = ""
-    for line in (r.stdout + r.stderr).splitlines():
+    for line in text.splitlines():
         m = re.search(r"Function properties for (\S+)", line)
         if m:
             cur = m.group(1)
         if re.search(r"[1-9]\d* bytes spill", line) or "warning" in line.lower():
             sys.stderr.write(f"{cur}: {line.strip()}\n")
-    regs = parse_ptxas(r.stdout + r.stderr)
+    regs = parse_ptxas(text)
     check_register_splits(regs)
     with open(REPORT, "w") as f:
         json.dump({"registers_per_thread": regs}, f, indent=1, sort_keys=True)

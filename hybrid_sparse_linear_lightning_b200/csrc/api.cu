@@ -15,6 +15,7 @@
 #include "block.cuh"
 #include "common.cuh"
 #include "decode.cuh"
+#include "host.cuh"
 #include "linear_simt.cuh"
 #include "linear_seg_tc.cuh"
 #include "prologue.cuh"
@@ -24,30 +25,10 @@
 #include "sparse_tc.cuh"
 
 #include <cublasLt.h>
-#include <cudaTypedefs.h>
 
 using namespace sala;
 
 namespace {
-
-constexpr size_t kAlign = 256;
-inline size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
-
-inline bool aligned16(const void* p) { return p && ((uintptr_t)p & 15u) == 0; }
-inline bool aligned16_or_null(const void* p) { return !p || ((uintptr_t)p & 15u) == 0; }
-
-std::atomic<uint64_t> g_launches{0};
-
-// Called once after every kernel launch: counts it and maps the launch error.
-inline sala_status launch_status() {
-  g_launches.fetch_add(1, std::memory_order_relaxed);
-  return cudaGetLastError() == cudaSuccess ? SALA_OK : SALA_ERR_CUDA;
-}
-
-template <typename K>
-inline cudaError_t allow_smem(K kernel, size_t bytes) {
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-}
 
 sala_status check_linear(const sala_linear_desc* d) {
   if (!d) return SALA_ERR_INVALID_ARG;
@@ -94,15 +75,6 @@ __global__ void selftest_unarrived_wait_kernel() {
   }
   __syncthreads();
   if (threadIdx.x == 0) (void)tc::mbar_wait(&bar, 0);
-}
-
-// base^(-2i/D) for i < D/2 in fp64
-RopeFreq rope_freq(int D, float base) {
-  RopeFreq rf;
-  memset(&rf, 0, sizeof(rf));
-  const double log2_base = log2((double)base);
-  for (int i = 0; i < D / 2; ++i) rf.inv[i] = exp2(-2.0 * i / D * log2_base);
-  return rf;
 }
 
 struct LinearWs {
@@ -179,15 +151,6 @@ sala_status run_select_begin(const sala_sparse_desc* d, const void* q, const voi
   return launch_status();
 }
 
-// SMs of the current device (cached per device).
-int device_sms() {
-  static int sms[64] = {};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-  if (!sms[dev]) cudaDeviceGetAttribute(&sms[dev], cudaDevAttrMultiProcessorCount, dev);
-  return sms[dev];
-}
-
 // Block-mean ranking of every query block from qsum and kbar.
 template <int D>
 sala_status run_select_finish(const sala_sparse_desc* d, const float* qsum, const float* kbar,
@@ -228,39 +191,6 @@ sala_status run_select(const sala_sparse_desc* d, const void* q, const void* k, 
     return launch_status();
   }
   return run_select_finish<D>(d, qsum, kbar, idx, st);
-}
-
-// cuTensorMapEncodeTiled through the runtime's driver entry point (no link
-// against libcuda).
-PFN_cuTensorMapEncodeTiled_v12000 get_encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) ==
-            cudaSuccess && q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  });
-  return fn;
-}
-
-// 2D bf16 view [rows, cols] (cols contiguous) loaded in boxes of
-// box_cols x box_rows.  With 128-byte swizzle and 64-column boxes one box
-// fills box_rows x 128 B of a K-major or MN-major MMA operand; with 64-byte
-// swizzle and 32-column boxes, box_rows x 64 B.
-bool make_tmap_bf16(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows,
-                    uint32_t box_cols = 64, uint32_t box_rows = 64,
-                    CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B) {
-  auto fn = get_encode_fn();
-  if (!fn) return false;
-  cuuint64_t dims[2] = {cols, rows};
-  cuuint64_t strides[1] = {cols * 2};
-  cuuint32_t box[2] = {box_cols, box_rows};
-  cuuint32_t estr[2] = {1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box,
-            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 sala_status run_linear_seg(const sala_linear_desc* d, const void* q, const void* k,
@@ -660,6 +590,12 @@ sala_status run_block(const sala_block_desc* b, const sala_linear_desc* lin,
 
 }  // namespace
 
+// The packed-batch translation unit keeps a status word of its own: OR of its
+// bits and the ones seen here.
+namespace sala {
+cudaError_t packed_take_status(unsigned* bits);
+}
+
 extern "C" {
 
 int sala_sparse_index_width(const sala_sparse_desc* d) {
@@ -880,6 +816,9 @@ sala_status sala_get_device_status(void* stream) {
   unsigned v = 0, zero = 0;
   if (cudaMemcpyFromSymbol(&v, g_status, sizeof(v)) != cudaSuccess) return SALA_ERR_CUDA;
   if (v && cudaMemcpyToSymbol(g_status, &zero, sizeof(zero)) != cudaSuccess) return SALA_ERR_CUDA;
+  unsigned pv = 0;
+  if (packed_take_status(&pv) != cudaSuccess) return SALA_ERR_CUDA;
+  v |= pv;
   if (v & kStatusTimeout) return SALA_ERR_TIMEOUT;
   if (v & kStatusBounds) return SALA_ERR_DEVICE_FAULT;
   return SALA_OK;

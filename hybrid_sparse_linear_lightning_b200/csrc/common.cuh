@@ -8,13 +8,14 @@
 namespace sala {
 
 // Per-device status word.  Kernels OR in these bits instead of trapping; the
-// host reads and clears it in sala_get_device_status().
+// host reads and clears it in sala_get_device_status().  Each translation unit
+// has a word of its own.
 enum : unsigned {
   kStatusTimeout = 1u,   // a bounded wait ran out of iterations
   kStatusBounds = 2u,    // an index check failed; the access was skipped
 };
 
-__device__ unsigned int g_status;
+static __device__ unsigned int g_status;
 
 __device__ __forceinline__ void set_status(unsigned bits) { atomicOr(&g_status, bits); }
 

@@ -1,0 +1,245 @@
+// Entry points for packed batches: prompts of different lengths in one call,
+// one token for each of many requests.
+#include <algorithm>
+#include <type_traits>
+
+#include "host.cuh"
+#include "packed_norm.cuh"
+#include "packed_simt.cuh"
+#include "packed_step.cuh"
+
+using namespace sala;
+
+namespace sala {
+// Reads and clears this translation unit's status word.
+cudaError_t packed_take_status(unsigned* bits) {
+  unsigned v = 0, zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(&v, g_status, sizeof(v));
+  if (e == cudaSuccess && v) e = cudaMemcpyToSymbol(g_status, &zero, sizeof(zero));
+  *bits = v;
+  return e;
+}
+}  // namespace sala
+
+namespace {
+
+using bf16 = __nv_bfloat16;
+
+inline bool dtype_ok(sala_dtype t) { return t == SALA_F32 || t == SALA_BF16; }
+inline bool dim_ok(int d) { return d == 64 || d == 128; }
+
+sala_status check_qk_norm(const sala_qk_norm_desc* d) {
+  if (!d || d->tokens < 1 || d->q_heads < 1 || d->k_heads < 1 || !dtype_ok(d->dtype))
+    return SALA_ERR_INVALID_ARG;
+  if (!(d->rms_eps >= 0.f) || !(d->rope_base > 0.f)) return SALA_ERR_INVALID_ARG;
+  if (!dim_ok(d->head_dim)) return SALA_ERR_UNSUPPORTED;
+  if ((int64_t)d->q_heads + d->k_heads > 8192) return SALA_ERR_UNSUPPORTED;
+  return SALA_OK;
+}
+
+// Head counts of grouped attention: a group's heads share the 128 rows of a
+// tensor-core tile.
+sala_status check_heads(int q_heads, int kv_heads, int head_dim) {
+  if (q_heads < 1 || kv_heads < 1 || q_heads % kv_heads != 0) return SALA_ERR_INVALID_ARG;
+  if (!dim_ok(head_dim) || q_heads / kv_heads > 128 || q_heads > 8192) return SALA_ERR_UNSUPPORTED;
+  return SALA_OK;
+}
+
+sala_status check_dense(const sala_dense_desc* d) {
+  if (!d || d->tokens < 1 || d->n_seqs < 1 || !dtype_ok(d->dtype) || !isfinite(d->scale))
+    return SALA_ERR_INVALID_ARG;
+  const sala_status s = check_heads(d->q_heads, d->kv_heads, d->head_dim);
+  if (s != SALA_OK) return s;
+  return d->dtype == SALA_BF16 ? SALA_OK : SALA_ERR_UNSUPPORTED;
+}
+
+sala_status check_packed_linear(const sala_packed_linear_desc* d) {
+  if (!d || d->tokens < 1 || d->n_seqs < 1 || d->n_slots < 1 || d->heads < 1 ||
+      !dtype_ok(d->dtype) || !isfinite(d->scale))
+    return SALA_ERR_INVALID_ARG;
+  if (!dim_ok(d->head_dim) || d->heads > 8192) return SALA_ERR_UNSUPPORTED;
+  return SALA_OK;
+}
+
+sala_status check_prefix(const sala_prefix_desc* d) {
+  if (!d || d->batch < 1 || d->prefix_len < 0 || d->n_slots < 1 || d->cache_capacity < 1 ||
+      !dtype_ok(d->dtype) || !isfinite(d->scale))
+    return SALA_ERR_INVALID_ARG;
+  const sala_status s = check_heads(d->q_heads, d->kv_heads, d->head_dim);
+  if (s != SALA_OK) return s;
+  // cache rows are addressed by 32-bit tile coordinates
+  if (d->cache_capacity * d->n_slots > 0x7fffffffll) return SALA_ERR_UNSUPPORTED;
+  return d->dtype == SALA_BF16 ? SALA_OK : SALA_ERR_UNSUPPORTED;
+}
+
+inline float softmax_scale(float scale, int head_dim) {
+  return scale > 0.f ? scale : 1.0f / sqrtf((float)head_dim);
+}
+
+template <typename T, int D>
+sala_status run_qk_norm(const sala_qk_norm_desc* d, const void* q, const void* k, const float* wq,
+                        const float* wk, const int32_t* pos, void* qn, void* kn, cudaStream_t st) {
+  // several tokens per CTA only where there are CTAs enough to fill the card
+  const int tpc = d->tokens >= 2048 ? kQkNormMaxTokens : 1;
+  qk_norm_kernel<T, D><<<(d->tokens + tpc - 1) / tpc, kQkNormThreads, 0, st>>>(
+      static_cast<const T*>(q), static_cast<const T*>(k), wq, wk, pos, static_cast<bf16*>(qn),
+      static_cast<bf16*>(kn), d->tokens, tpc, d->q_heads, d->k_heads, rope_freq(D, d->rope_base),
+      d->rms_eps);
+  return launch_status();
+}
+
+template <typename T, int D>
+sala_status run_step(const sala_packed_linear_desc* d, const void* q, const void* k, const void* v,
+                     const void* gate, const float* lambda, const int32_t* slots, float* state,
+                     void* out, cudaStream_t st) {
+  const long long units = (long long)d->n_seqs * d->heads;
+  auto launch = [&](auto kern, int split) {
+    kern<<<(unsigned)(units * split), kStepThreads, 0, st>>>(
+        static_cast<const bf16*>(q), static_cast<const bf16*>(k), static_cast<const T*>(v),
+        static_cast<const T*>(gate), lambda, slots, state, static_cast<T*>(out), d->heads,
+        d->n_slots, d->scale);
+    return launch_status();
+  };
+  if (units < 4 * std::max(device_sms(), 1)) return launch(linear_step_kernel<T, D, 32>, D / 32);
+  return launch(linear_step_kernel<T, D, D>, 1);
+}
+
+}  // namespace
+
+extern "C" {
+
+sala_status sala_qk_norm(const sala_qk_norm_desc* d, const void* q, const void* k, const float* wq,
+                         const float* wk, const int32_t* positions, void* q_norm, void* k_norm,
+                         void* stream) {
+  const sala_status s = check_qk_norm(d);
+  if (s != SALA_OK) return s;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(wq) || !aligned16(wk) || !aligned16(q_norm) ||
+      !aligned16(k_norm) || !aligned16_or_null(positions))
+    return SALA_ERR_INVALID_ARG;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (d->dtype == SALA_BF16) {
+    if (d->head_dim == 128) return run_qk_norm<bf16, 128>(d, q, k, wq, wk, positions, q_norm, k_norm, st);
+    return run_qk_norm<bf16, 64>(d, q, k, wq, wk, positions, q_norm, k_norm, st);
+  }
+  if (d->head_dim == 128) return run_qk_norm<float, 128>(d, q, k, wq, wk, positions, q_norm, k_norm, st);
+  return run_qk_norm<float, 64>(d, q, k, wq, wk, positions, q_norm, k_norm, st);
+}
+
+size_t sala_dense_workspace_size(const sala_dense_desc* d) {
+  if (check_dense(d) != SALA_OK) return 0;
+  return 0;
+}
+
+sala_status sala_dense_prefill(const sala_dense_desc* d, const void* q_norm, const void* k_norm,
+                               const void* v, const void* gate, const int32_t* cu_seqlens,
+                               void* out, void* workspace, size_t ws_bytes, void* stream) {
+  const sala_status s = check_dense(d);
+  if (s != SALA_OK) return s;
+  if (!aligned16(q_norm) || !aligned16(k_norm) || !aligned16(v) || !aligned16(gate) ||
+      !aligned16(cu_seqlens) || !aligned16(out))
+    return SALA_ERR_INVALID_ARG;
+  (void)workspace;
+  (void)ws_bytes;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const float sl2 = softmax_scale(d->scale, d->head_dim) * 1.4426950408889634f;
+  const long long rows = (long long)d->tokens * d->q_heads;
+  auto launch = [&](auto kern) {
+    kern<<<(unsigned)((rows + kPkSimtWarps - 1) / kPkSimtWarps), 32 * kPkSimtWarps, 0, st>>>(
+        static_cast<const bf16*>(q_norm), static_cast<const bf16*>(k_norm),
+        static_cast<const bf16*>(v), static_cast<const bf16*>(gate), cu_seqlens,
+        static_cast<bf16*>(out), d->tokens, d->n_seqs, d->q_heads, d->kv_heads, sl2);
+    return launch_status();
+  };
+  return d->head_dim == 128 ? launch(dense_simt_kernel<128>) : launch(dense_simt_kernel<64>);
+}
+
+size_t sala_linear_packed_workspace_size(const sala_packed_linear_desc* d) {
+  if (check_packed_linear(d) != SALA_OK) return 0;
+  return 0;
+}
+
+sala_status sala_linear_packed_prefill(const sala_packed_linear_desc* d, const void* q_norm,
+                                       const void* k_norm, const void* v, const void* gate,
+                                       const float* lambda, const int32_t* cu_seqlens,
+                                       const int32_t* slots, const float* state_in,
+                                       float* state_out, void* out, void* workspace,
+                                       size_t ws_bytes, void* stream) {
+  const sala_status s = check_packed_linear(d);
+  if (s != SALA_OK) return s;
+  if (d->dtype != SALA_BF16) return SALA_ERR_UNSUPPORTED;
+  if (!aligned16(q_norm) || !aligned16(k_norm) || !aligned16(v) || !aligned16(gate) ||
+      !aligned16(lambda) || !aligned16(cu_seqlens) || !aligned16_or_null(slots) ||
+      !aligned16_or_null(state_in) || !aligned16_or_null(state_out) || !aligned16(out))
+    return SALA_ERR_INVALID_ARG;
+  if (!slots && d->n_slots < d->n_seqs) return SALA_ERR_INVALID_ARG;
+  (void)workspace;
+  (void)ws_bytes;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  auto launch = [&](auto kern, int D) {
+    kern<<<(unsigned)((long long)d->n_seqs * d->heads * (D / 32)), 256, 0, st>>>(
+        static_cast<const bf16*>(q_norm), static_cast<const bf16*>(k_norm),
+        static_cast<const bf16*>(v), static_cast<const bf16*>(gate), lambda, cu_seqlens, slots,
+        state_in, state_out, static_cast<bf16*>(out), d->tokens, d->heads, d->n_slots, d->scale);
+    return launch_status();
+  };
+  return d->head_dim == 128 ? launch(linear_packed_simt_kernel<128>, 128)
+                            : launch(linear_packed_simt_kernel<64>, 64);
+}
+
+sala_status sala_linear_packed_step(const sala_packed_linear_desc* d, const void* q_norm,
+                                    const void* k_norm, const void* v, const void* gate,
+                                    const float* lambda, const int32_t* slots, float* state,
+                                    void* out, void* stream) {
+  const sala_status s = check_packed_linear(d);
+  if (s != SALA_OK) return s;
+  if (d->tokens != d->n_seqs) return SALA_ERR_INVALID_ARG;
+  if (!aligned16(q_norm) || !aligned16(k_norm) || !aligned16(v) || !aligned16(gate) ||
+      !aligned16(lambda) || !aligned16_or_null(slots) || !aligned16(state) || !aligned16(out))
+    return SALA_ERR_INVALID_ARG;
+  if (!slots && d->n_slots < d->n_seqs) return SALA_ERR_INVALID_ARG;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (d->dtype == SALA_BF16) {
+    if (d->head_dim == 128) return run_step<bf16, 128>(d, q_norm, k_norm, v, gate, lambda, slots, state, out, st);
+    return run_step<bf16, 64>(d, q_norm, k_norm, v, gate, lambda, slots, state, out, st);
+  }
+  if (d->head_dim == 128) return run_step<float, 128>(d, q_norm, k_norm, v, gate, lambda, slots, state, out, st);
+  return run_step<float, 64>(d, q_norm, k_norm, v, gate, lambda, slots, state, out, st);
+}
+
+size_t sala_prefix_workspace_size(const sala_prefix_desc* d) {
+  if (check_prefix(d) != SALA_OK) return 0;
+  return 0;
+}
+
+sala_status sala_prefix_decode(const sala_prefix_desc* d, const void* q_norm, const void* k_norm,
+                               const void* v, const void* gate, const void* prefix_k,
+                               const void* prefix_v, void* k_cache, void* v_cache,
+                               const int32_t* lens, const int32_t* slots, void* out,
+                               void* workspace, size_t ws_bytes, void* stream) {
+  const sala_status s = check_prefix(d);
+  if (s != SALA_OK) return s;
+  if (!aligned16(q_norm) || !aligned16(k_norm) || !aligned16(v) || !aligned16(gate) ||
+      !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(lens) || !aligned16_or_null(slots) ||
+      !aligned16(out))
+    return SALA_ERR_INVALID_ARG;
+  if (d->prefix_len > 0 && (!aligned16(prefix_k) || !aligned16(prefix_v))) return SALA_ERR_INVALID_ARG;
+  if (!slots && d->n_slots < d->batch) return SALA_ERR_INVALID_ARG;
+  (void)workspace;
+  (void)ws_bytes;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const float sl2 = softmax_scale(d->scale, d->head_dim) * 1.4426950408889634f;
+  auto launch = [&](auto kern) {
+    const dim3 grid((d->q_heads + kPkSimtWarps - 1) / kPkSimtWarps, d->batch);
+    kern<<<grid, 32 * kPkSimtWarps, 0, st>>>(
+        static_cast<const bf16*>(q_norm), static_cast<const bf16*>(k_norm),
+        static_cast<const bf16*>(v), static_cast<const bf16*>(gate),
+        static_cast<const bf16*>(prefix_k), static_cast<const bf16*>(prefix_v),
+        static_cast<bf16*>(k_cache), static_cast<bf16*>(v_cache), lens, slots,
+        static_cast<bf16*>(out), d->q_heads, d->kv_heads, d->prefix_len,
+        (long long)d->cache_capacity, d->n_slots, sl2);
+    return launch_status();
+  };
+  return d->head_dim == 128 ? launch(prefix_simt_kernel<128>) : launch(prefix_simt_kernel<64>);
+}
+
+}  // extern "C"

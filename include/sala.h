@@ -31,7 +31,8 @@
  *     (a bounded wait that ran out, an index out of range) set a per-device
  *     status word that sala_get_device_status() returns and clears.
  *   - Supported shapes: head_dim in {64, 128}; seqlen a multiple of the linear
- *     chunk and of the sparse block (64); q_heads a multiple of kv_heads.
+ *     chunk and of the sparse block (64); q_heads a multiple of kv_heads.  The
+ *     calls for packed batches take sequences of any length.
  */
 #ifndef SALA_H_
 #define SALA_H_
@@ -299,6 +300,128 @@ size_t sala_decode_workspace_size(const sala_decode_desc* d);
 sala_status sala_decode_step(const sala_decode_desc* d, const sala_decode_io* io,
                              void* k_cache, void* v_cache, float* kbar, float* ksum,
                              int64_t cur_len, void* workspace, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------- packed batches */
+
+/* Serving calls: prompts of different lengths in one call, then one token of
+ * each of many requests (no counterpart on the pages, which run one sequence:
+ * the same layers for a batch whose requests differ in length).
+ *   - Packed tokens: rows of all prompts one behind the other, [tokens, heads,
+ *     d] with no padding.  cu_seqlens: [n_seqs + 1] int32 on the device,
+ *     ascending; sequence i owns rows [cu_seqlens[i], cu_seqlens[i + 1]).
+ *     Lengths need be multiples of nothing; 0 and 1 are lengths.  Rows before
+ *     the first sequence and behind the last one are neither read for another
+ *     row's result nor written.  A sequence whose bounds descend or leave
+ *     [0, tokens] is skipped and sets the bounds bit of the status word.
+ *   - Sequences are isolated: whatever one holds (NaN and infinities too), the
+ *     others' results do not change; nor do those of a sequence's own earlier
+ *     tokens.
+ *   - Slots: per-request state and caches live in pools of n_slots entries;
+ *     slots [n] int32 names the entry of each sequence (row).  NULL: entry i
+ *     for sequence i (n_slots >= n).  A negative slot marks a padded row,
+ *     which is skipped: nothing of it is written.  A slot >= n_slots, or one
+ *     that an earlier row of the call names too, is skipped likewise and sets
+ *     the bounds bit.
+ *   - The calls read lengths and slots on the device only, so a call captured
+ *     into a CUDA graph follows what these arrays hold at replay.  Two calls
+ *     that may overlap on the GPU (captured graphs among them) need a
+ *     workspace each.
+ *   - q_norm and k_norm are bf16 whatever the dtype, as everywhere here. */
+
+/* QK-RMSNorm of packed tokens and, with positions, RoPE: what
+ * sala_linear_prefill and sala_sparse_select do to q and k first. */
+typedef struct {
+  int tokens, q_heads, k_heads, head_dim;
+  sala_dtype dtype;          /* of q and k                                     */
+  float rope_base, rms_eps;
+} sala_qk_norm_desc;
+
+/* In:  q [tokens, q_heads, d], k [tokens, k_heads, d] of d->dtype; wq, wk [d]
+ *      fp32; positions [tokens] int32, or NULL for no RoPE (sparse layers).
+ * Out: q_norm, k_norm bf16 of the same shapes; q_norm may be q and k_norm may
+ *      be k where these are bf16.  No workspace. */
+sala_status sala_qk_norm(const sala_qk_norm_desc* d, const void* q, const void* k,
+                         const float* wq, const float* wk, const int32_t* positions,
+                         void* q_norm, void* k_norm, void* stream);
+
+/* The sparse layer's dense form: every query attends to all keys of its
+ * sequence up to itself (what the block selection comes to for prompts that
+ * fit into the selected blocks).  q_heads / kv_heads up to 128; SALA_BF16. */
+typedef struct {
+  int tokens, n_seqs, q_heads, kv_heads, head_dim;
+  sala_dtype dtype;
+  float scale;               /* <= 0 selects 1/sqrt(head_dim)                  */
+} sala_dense_desc;
+
+size_t sala_dense_workspace_size(const sala_dense_desc* d);
+
+/* out = sigmoid(gate) * softmax(scale q k^T, causal) v per sequence and head.
+ * q_norm [tokens, q_heads, d], k_norm, v [tokens, kv_heads, d], gate, out
+ * [tokens, q_heads, d].  out must not overlap the inputs. */
+sala_status sala_dense_prefill(const sala_dense_desc* d, const void* q_norm, const void* k_norm,
+                               const void* v, const void* gate, const int32_t* cu_seqlens,
+                               void* out, void* workspace, size_t ws_bytes, void* stream);
+
+/* Linear layer on packed tokens.  Takes q and k as sala_qk_norm leaves them:
+ *   S_t = lambda_h S_{t-1} + k_t^T v_t,  out_t = sigmoid(gate_t) * scale * q_t S_t */
+typedef struct {
+  int tokens, n_seqs, n_slots, heads, head_dim;
+  sala_dtype dtype;          /* of v, gate and out                             */
+  float scale;
+} sala_packed_linear_desc;
+
+size_t sala_linear_packed_workspace_size(const sala_packed_linear_desc* d);
+
+/* Prompts (SALA_BF16).  state_in: pool [n_slots, heads, d, d] fp32 of the
+ * states the sequences start from, or NULL for zeros; state_out: pool of the
+ * states they end with, or NULL; it may be state_in.  Entries that no
+ * sequence names are left as they are; a sequence of length 0 hands its state
+ * on.  A padded sequence (negative slot) starts from zeros, and its tokens'
+ * outputs are written. lambda in [0, 1]. */
+sala_status sala_linear_packed_prefill(const sala_packed_linear_desc* d, const void* q_norm,
+                                       const void* k_norm, const void* v, const void* gate,
+                                       const float* lambda, const int32_t* cu_seqlens,
+                                       const int32_t* slots, const float* state_in,
+                                       float* state_out, void* out, void* workspace,
+                                       size_t ws_bytes, void* stream);
+
+/* One token of each of n_seqs requests (tokens == n_seqs; row i of q_norm,
+ * k_norm, v, gate and out belongs to slots[i]); the states are updated in
+ * place.  SALA_F32 or SALA_BF16.  No workspace. */
+sala_status sala_linear_packed_step(const sala_packed_linear_desc* d, const void* q_norm,
+                                    const void* k_norm, const void* v, const void* gate,
+                                    const float* lambda, const int32_t* slots, float* state,
+                                    void* out, void* stream);
+
+/* One decode token of each of `batch` requests that share their first
+ * prefix_len tokens, through the sparse layer's dense form: the prefix's keys
+ * and values are read once for the whole batch.  SALA_BF16; q_heads /
+ * kv_heads up to 128. */
+typedef struct {
+  int batch, prefix_len;     /* prefix_len >= 0                                */
+  int n_slots, q_heads, kv_heads, head_dim;
+  int64_t cache_capacity;    /* token rows per slot of k_cache / v_cache       */
+  sala_dtype dtype;
+  float scale;               /* <= 0 selects 1/sqrt(head_dim)                  */
+} sala_prefix_desc;
+
+size_t sala_prefix_workspace_size(const sala_prefix_desc* d);
+
+/* q_norm, gate, out [batch, q_heads, d]; k_norm, v [batch, kv_heads, d]: the
+ * new token.  prefix_k, prefix_v [prefix_len, kv_heads, d] (may be NULL when
+ * prefix_len is 0): normalised keys / raw values, the k_norm and v of a
+ * prefill.  k_cache, v_cache [n_slots, cache_capacity, kv_heads, d] bf16: what
+ * each request holds behind the prefix; lens [batch] int32: how many rows of
+ * its entry request i holds, in [0, cache_capacity).  Request i attends to the
+ * prefix, rows [0, lens[i]) of its entry and its new token, which the call
+ * appends as row lens[i] (the caller advances lens).  Rows at and behind
+ * lens[i] are not read for the result: they may hold anything.  A length out
+ * of range skips the row and sets the bounds bit. */
+sala_status sala_prefix_decode(const sala_prefix_desc* d, const void* q_norm, const void* k_norm,
+                               const void* v, const void* gate, const void* prefix_k,
+                               const void* prefix_v, void* k_cache, void* v_cache,
+                               const int32_t* lens, const int32_t* slots, void* out,
+                               void* workspace, size_t ws_bytes, void* stream);
 
 /* -------------------------------------------------------------------- misc */
 
