@@ -47,6 +47,7 @@ def needs_build() -> bool:
 # this many registers per thread, so a library that built cannot hang on a
 # register split larger than its launch allocation.
 REGISTER_SPLIT_KERNELS = {"linear_segout_kernel": 128}
+PACKED_SPLIT_KERNELS = {"dense_attn_kernel": 168}
 REPORT = os.path.join(PKG, "libsala.ptxas.json")
 
 
@@ -65,8 +66,8 @@ def parse_ptxas(text: str) -> dict:
     return regs
 
 
-def check_register_splits(regs: dict) -> None:
-    for short, want in REGISTER_SPLIT_KERNELS.items():
+def check_register_splits(regs: dict, splits: dict = REGISTER_SPLIT_KERNELS) -> None:
+    for short, want in splits.items():
         got = {k: v for k, v in regs.items() if short in k}
         if not got:
             raise RuntimeError(f"ptxas report has no entry for {short}")
@@ -109,6 +110,7 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
             sys.stderr.write(f"{cur}: {line.strip()}\n")
     regs = parse_ptxas(text)
     check_register_splits(regs)
+    check_register_splits(regs, PACKED_SPLIT_KERNELS)
     with open(REPORT, "w") as f:
         json.dump({"registers_per_thread": regs}, f, indent=1, sort_keys=True)
     os.replace(LIB + ".tmp", LIB)

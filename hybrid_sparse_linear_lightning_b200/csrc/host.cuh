@@ -86,4 +86,19 @@ inline bool make_tmap_bf16(CUtensorMap* map, const void* base, uint64_t cols, ui
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// 3D bf16 view [tokens, heads, D]: boxes of 64 columns x box_heads x
+// box_tokens, rows of 128 bytes ordered by token, then head (128-byte swizzle).
+inline bool make_tmap_rows(CUtensorMap* map, const void* base, uint64_t D, uint64_t heads, uint64_t tokens,
+                           uint32_t box_heads, uint32_t box_tokens) {
+  auto fn = get_encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {D, heads, tokens};
+  cuuint64_t strides[2] = {D * 2, heads * D * 2};
+  cuuint32_t box[3] = {64, box_heads, box_tokens};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace sala

@@ -4,6 +4,7 @@
 #include <type_traits>
 
 #include "host.cuh"
+#include "packed_attn.cuh"
 #include "packed_norm.cuh"
 #include "packed_simt.cuh"
 #include "packed_step.cuh"
@@ -104,6 +105,28 @@ sala_status run_step(const sala_packed_linear_desc* d, const void* q, const void
   return launch(linear_step_kernel<T, D, D>, 1);
 }
 
+template <int D>
+sala_status run_dense(const sala_dense_desc* d, const void* q, const void* k, const void* v,
+                      const void* gate, const int32_t* cu, void* out, float sl2, cudaStream_t st) {
+  const int G = d->q_heads / d->kv_heads, Tt = 128 / G;
+  CUtensorMap qm, km, vm;
+  const uint64_t kv_cols = (uint64_t)d->kv_heads * D;
+  if (!make_tmap_rows(&qm, q, D, d->q_heads, d->tokens, G, Tt) ||
+      !make_tmap_bf16(&km, k, kv_cols, d->tokens, 64, kPaBlock) ||
+      !make_tmap_bf16(&vm, v, kv_cols, d->tokens, 64, kPaBlock))
+    return SALA_ERR_CUDA;
+  auto kern = dense_attn_kernel<D>;
+  const size_t smem = PaLayout<D>::kBytes + 1024;
+  if (allow_smem(kern, smem) != cudaSuccess) return SALA_ERR_CUDA;
+  // every sequence ends in a pair of tiles that may be part empty
+  const int64_t pairs = (int64_t)d->tokens / (2 * Tt) + d->n_seqs;
+  if (pairs * d->kv_heads > 0x7fffffffll) return SALA_ERR_UNSUPPORTED;
+  kern<<<(unsigned)(pairs * d->kv_heads), kPaThreads, smem, st>>>(
+      qm, km, vm, cu, static_cast<const bf16*>(v), static_cast<const bf16*>(gate),
+      static_cast<bf16*>(out), d->tokens, d->n_seqs, d->q_heads, d->kv_heads, Tt, sl2);
+  return launch_status();
+}
+
 }  // namespace
 
 extern "C" {
@@ -142,15 +165,8 @@ sala_status sala_dense_prefill(const sala_dense_desc* d, const void* q_norm, con
   (void)ws_bytes;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const float sl2 = softmax_scale(d->scale, d->head_dim) * 1.4426950408889634f;
-  const long long rows = (long long)d->tokens * d->q_heads;
-  auto launch = [&](auto kern) {
-    kern<<<(unsigned)((rows + kPkSimtWarps - 1) / kPkSimtWarps), 32 * kPkSimtWarps, 0, st>>>(
-        static_cast<const bf16*>(q_norm), static_cast<const bf16*>(k_norm),
-        static_cast<const bf16*>(v), static_cast<const bf16*>(gate), cu_seqlens,
-        static_cast<bf16*>(out), d->tokens, d->n_seqs, d->q_heads, d->kv_heads, sl2);
-    return launch_status();
-  };
-  return d->head_dim == 128 ? launch(dense_simt_kernel<128>) : launch(dense_simt_kernel<64>);
+  if (d->head_dim == 128) return run_dense<128>(d, q_norm, k_norm, v, gate, cu_seqlens, out, sl2, st);
+  return run_dense<64>(d, q_norm, k_norm, v, gate, cu_seqlens, out, sl2, st);
 }
 
 size_t sala_linear_packed_workspace_size(const sala_packed_linear_desc* d) {

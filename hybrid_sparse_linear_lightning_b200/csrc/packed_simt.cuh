@@ -3,6 +3,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "packed_attn.cuh"
 #include "packed_step.cuh"
 
 namespace sala {
@@ -45,51 +46,6 @@ struct RowSoftmax {
     }
   }
 };
-
-// Sequence of packed row t, from cu_seqlens (n + 1 ascending starts); -1 where
-// none holds it.
-__device__ __forceinline__ int find_seq(const int32_t* cu, int n, int t) {
-  int lo = 0, hi = n;
-  while (lo < hi) {          // first i with cu[i + 1] > t
-    const int mid = (lo + hi) >> 1;
-    if (cu[mid + 1] > t) hi = mid; else lo = mid + 1;
-  }
-  return lo < n && cu[lo] <= t ? lo : -1;
-}
-
-__device__ __forceinline__ bool seq_ok(const int32_t* cu, int i, int tokens) {
-  return cu[i] >= 0 && cu[i] <= cu[i + 1] && cu[i + 1] <= tokens;
-}
-
-template <int D>
-__global__ void __launch_bounds__(32 * kPkSimtWarps)
-dense_simt_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __restrict__ k,
-                  const __nv_bfloat16* __restrict__ v, const __nv_bfloat16* __restrict__ gate,
-                  const int32_t* __restrict__ cu, __nv_bfloat16* __restrict__ out, int tokens,
-                  int n_seqs, int Hq, int Hkv, float sl2) {
-  __shared__ float qs[kPkSimtWarps][D];
-  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long row = (long long)blockIdx.x * kPkSimtWarps + w;
-  if (blockIdx.x == 0)
-    for (int i = threadIdx.x; i < n_seqs; i += blockDim.x)
-      if (!seq_ok(cu, i, tokens)) set_status(kStatusBounds);
-  if (row >= (long long)tokens * Hq) return;
-  const int t = (int)(row / Hq), h = (int)(row % Hq), g = h / (Hq / Hkv);
-  const int s = find_seq(cu, n_seqs, t);
-  if (s < 0 || !seq_ok(cu, s, tokens)) return;
-  const int s0 = cu[s];
-  constexpr int E = D / 32;
-  for (int e = 0; e < E; ++e) qs[w][lane * E + e] = to_f32(q[row * D + lane * E + e]);
-  __syncwarp();
-  RowSoftmax<D> a;
-  const long long st = (long long)Hkv * D;
-  for (int j = s0; j <= t; j += 32)
-    a.add(qs[w], k + j * st + g * D, v + j * st + g * D, st, min(32, t + 1 - j), sl2);
-  for (int e = 0; e < E; ++e) {
-    const long long at = row * D + lane * E + e;
-    out[at] = __float2bfloat16_rn(sigmoidf_(to_f32(gate[at])) * a.o[e] / a.l);
-  }
-}
 
 template <int D>
 __global__ void __launch_bounds__(32 * kPkSimtWarps)
