@@ -5,6 +5,7 @@
 
 #include "host.cuh"
 #include "packed_attn.cuh"
+#include "packed_decode.cuh"
 #include "packed_norm.cuh"
 #include "packed_simt.cuh"
 #include "packed_step.cuh"
@@ -127,6 +128,99 @@ sala_status run_dense(const sala_dense_desc* d, const void* q, const void* k, co
   return launch_status();
 }
 
+// How a decode step over a shared prefix is cut up.
+struct PrefixPlan {
+  int Tt, pairs;                 // requests per row tile, pairs of row tiles
+  int split_blocks, n_split;     // key blocks per part of the prefix, parts
+  size_t o, ml, total;           // workspace: parts of O, of (maximum, sum)
+};
+
+PrefixPlan prefix_plan(const sala_prefix_desc* d) {
+  constexpr int kSms = 148;
+  PrefixPlan p = {};
+  p.Tt = 128 / (d->q_heads / d->kv_heads);
+  const int64_t tiles = ((int64_t)d->batch + p.Tt - 1) / p.Tt;
+  p.pairs = (int)((tiles + 1) / 2);
+  const int64_t blocks = ((int64_t)d->prefix_len + kPaBlock - 1) / kPaBlock;
+  if (blocks > 0) {
+    // the number of parts whose waves of units take the fewest block times; a
+    // unit costs two blocks' time to start and to hand over its part
+    const int64_t units = d->kv_heads * (int64_t)p.pairs;
+    int64_t best = INT64_MAX;
+    for (int64_t n = 1; n <= std::min<int64_t>(blocks, kOwnMaxSplits); ++n) {
+      const int64_t per = (blocks + n - 1) / n;
+      const int64_t cost = ((units * n + kSms - 1) / kSms) * (per + 2);
+      if (cost < best) {
+        best = cost;
+        p.split_blocks = (int)per;
+      }
+    }
+    p.n_split = (int)((blocks + p.split_blocks - 1) / p.split_blocks);
+  }
+  const size_t rows = (size_t)p.n_split * d->batch * d->q_heads;
+  p.o = 0;
+  p.ml = align_up(rows * d->head_dim * sizeof(float));
+  p.total = rows ? p.ml + align_up(rows * sizeof(float2)) : 0;
+  return p;
+}
+
+template <int D>
+sala_status run_prefix(const sala_prefix_desc* d, const void* q, const void* k, const void* v,
+                       const void* gate, const void* pk, const void* pv, void* kc, void* vc,
+                       const int32_t* lens, const int32_t* slots, void* out, uint8_t* ws,
+                       cudaStream_t st) {
+  const PrefixPlan p = prefix_plan(d);
+  const float sl2 = softmax_scale(d->scale, D) * 1.4426950408889634f;
+  float* part_o = reinterpret_cast<float*>(ws + p.o);
+  float2* part_ml = reinterpret_cast<float2*>(ws + p.ml);
+  const int G = d->q_heads / d->kv_heads;
+  if (p.n_split > 0) {
+    CUtensorMap qm, km, vm;
+    const uint64_t kv_cols = (uint64_t)d->kv_heads * D;
+    if (!make_tmap_rows(&qm, q, D, d->q_heads, d->batch, G, p.Tt) ||
+        !make_tmap_bf16(&km, pk, kv_cols, d->prefix_len, 64, kPaBlock) ||
+        !make_tmap_bf16(&vm, pv, kv_cols, d->prefix_len, 64, kPaBlock))
+      return SALA_ERR_CUDA;
+    const size_t smem = PaLayout<D>::kBytes + 1024;
+    if (allow_smem(prefix_attn_kernel<D>, smem) != cudaSuccess) return SALA_ERR_CUDA;
+    const int64_t units = (int64_t)p.n_split * p.pairs * d->kv_heads;
+    prefix_attn_kernel<D><<<(unsigned)units, kPaThreads, smem, st>>>(
+        qm, km, vm, part_o, part_ml, d->batch, d->q_heads, d->kv_heads, p.Tt, p.pairs, d->prefix_len,
+        p.split_blocks, sl2);
+    const sala_status s = launch_status();
+    if (s != SALA_OK) return s;
+  }
+  // clusters grow until their CTAs fill the card twice over (two CTAs live on an
+  // SM), as long as every warp still has keys of a full cache
+  const int mtiles = (G + 15) / 16;
+  const int64_t units = (int64_t)d->batch * d->kv_heads * mtiles;
+  int cs = 1;
+  while (cs < kOwnMaxCluster && units * cs < 4 * 148 && d->cache_capacity > (int64_t)cs * kOwnWarps * 16) cs *= 2;
+  if (units * cs > 0x7fffffffll) return SALA_ERR_UNSUPPORTED;
+  auto kern = own_attn_kernel<D>;
+  const size_t smem = OwnLayout<D>::kBytes;
+  if (allow_smem(kern, smem) != cudaSuccess) return SALA_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(units * cs));
+  cfg.blockDim = dim3(32 * kOwnWarps);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cs;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.n_split > 0 ? 2 : 1;    // alone, the kernel starts after what came before it
+  cudaLaunchKernelEx(&cfg, kern, static_cast<const bf16*>(q), static_cast<const bf16*>(k),
+                     static_cast<const bf16*>(v), static_cast<const bf16*>(gate), static_cast<bf16*>(kc),
+                     static_cast<bf16*>(vc), lens, slots, static_cast<const float*>(part_o),
+                     static_cast<const float2*>(part_ml), static_cast<bf16*>(out), d->batch, d->q_heads,
+                     d->kv_heads, mtiles, p.n_split, (long long)d->cache_capacity, d->n_slots, sl2);
+  return launch_status();
+}
+
 }  // namespace
 
 extern "C" {
@@ -224,7 +318,7 @@ sala_status sala_linear_packed_step(const sala_packed_linear_desc* d, const void
 
 size_t sala_prefix_workspace_size(const sala_prefix_desc* d) {
   if (check_prefix(d) != SALA_OK) return 0;
-  return 0;
+  return prefix_plan(d).total;
 }
 
 sala_status sala_prefix_decode(const sala_prefix_desc* d, const void* q_norm, const void* k_norm,
@@ -240,22 +334,14 @@ sala_status sala_prefix_decode(const sala_prefix_desc* d, const void* q_norm, co
     return SALA_ERR_INVALID_ARG;
   if (d->prefix_len > 0 && (!aligned16(prefix_k) || !aligned16(prefix_v))) return SALA_ERR_INVALID_ARG;
   if (!slots && d->n_slots < d->batch) return SALA_ERR_INVALID_ARG;
-  (void)workspace;
-  (void)ws_bytes;
+  const size_t need = prefix_plan(d).total;
+  if (need > 0 && (!workspace || ws_bytes < need)) return SALA_ERR_WORKSPACE;
+  if (need > 0 && !aligned16(workspace)) return SALA_ERR_INVALID_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const float sl2 = softmax_scale(d->scale, d->head_dim) * 1.4426950408889634f;
-  auto launch = [&](auto kern) {
-    const dim3 grid((d->q_heads + kPkSimtWarps - 1) / kPkSimtWarps, d->batch);
-    kern<<<grid, 32 * kPkSimtWarps, 0, st>>>(
-        static_cast<const bf16*>(q_norm), static_cast<const bf16*>(k_norm),
-        static_cast<const bf16*>(v), static_cast<const bf16*>(gate),
-        static_cast<const bf16*>(prefix_k), static_cast<const bf16*>(prefix_v),
-        static_cast<bf16*>(k_cache), static_cast<bf16*>(v_cache), lens, slots,
-        static_cast<bf16*>(out), d->q_heads, d->kv_heads, d->prefix_len,
-        (long long)d->cache_capacity, d->n_slots, sl2);
-    return launch_status();
-  };
-  return d->head_dim == 128 ? launch(prefix_simt_kernel<128>) : launch(prefix_simt_kernel<64>);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  if (d->head_dim == 128)
+    return run_prefix<128>(d, q_norm, k_norm, v, gate, prefix_k, prefix_v, k_cache, v_cache, lens, slots, out, ws, st);
+  return run_prefix<64>(d, q_norm, k_norm, v, gate, prefix_k, prefix_v, k_cache, v_cache, lens, slots, out, ws, st);
 }
 
 }  // extern "C"
