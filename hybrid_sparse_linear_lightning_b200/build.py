@@ -47,7 +47,8 @@ def needs_build() -> bool:
 # this many registers per thread, so a library that built cannot hang on a
 # register split larger than its launch allocation.
 REGISTER_SPLIT_KERNELS = {"linear_segout_kernel": 128}
-PACKED_SPLIT_KERNELS = {"dense_attn_kernel": 168, "prefix_attn_kernel": 168}
+PACKED_SPLIT_KERNELS = {"dense_attn_kernel": 168, "prefix_attn_kernel": 168,
+                        "linear_packed_kernel": 128}
 REPORT = os.path.join(PKG, "libsala.ptxas.json")
 
 

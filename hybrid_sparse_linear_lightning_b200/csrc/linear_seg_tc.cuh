@@ -157,20 +157,6 @@ __device__ __forceinline__ void sw128_norm_rope_row(uint8_t* tile, int r, const 
   }
 }
 
-// 32 fp32 values -> bf16 columns [32 j, 32 j + 32) of row r of the same layout.
-__device__ __forceinline__ void sw128_store_row32(uint8_t* tile, int r, int j, const float* v) {
-  uint8_t* atom = tile + (j >> 1) * 16384 + r * 128;
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const int ch = (j & 1) * 4 + q;
-    uint4 u;
-    __nv_bfloat162* h2 = reinterpret_cast<__nv_bfloat162*>(&u);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) h2[e] = __floats2bfloat162_rn(v[q * 8 + 2 * e], v[q * 8 + 2 * e + 1]);
-    *reinterpret_cast<uint4*>(atom + ((ch ^ (r & 7)) << 4)) = u;
-  }
-}
-
 // --------------------------------------------------------------------------
 // 1. Segment sums
 // --------------------------------------------------------------------------

@@ -7,7 +7,7 @@
 #include "packed_attn.cuh"
 #include "packed_decode.cuh"
 #include "packed_norm.cuh"
-#include "packed_simt.cuh"
+#include "packed_linear.cuh"
 #include "packed_step.cuh"
 
 using namespace sala;
@@ -126,6 +126,67 @@ sala_status run_dense(const sala_dense_desc* d, const void* q, const void* k, co
       qm, km, vm, cu, static_cast<const bf16*>(v), static_cast<const bf16*>(gate),
       static_cast<bf16*>(out), d->tokens, d->n_seqs, d->q_heads, d->kv_heads, Tt, sl2);
   return launch_status();
+}
+
+// How packed prompts are cut for linear attention.
+struct LinearPlan {
+  int seg_tokens;
+  int64_t extra;        // most segments behind a sequence's first
+  size_t total;         // workspace: states that enter them
+};
+
+LinearPlan linear_plan(const sala_packed_linear_desc* d) {
+  constexpr int64_t kSms = 148;
+  LinearPlan p;
+  const int64_t groups = (d->heads + 128 / d->head_dim - 1) / (128 / d->head_dim);
+  const int64_t tiles = ((int64_t)d->tokens + kPlTile - 1) / kPlTile * groups;
+  // four CTAs per SM by cutting; with many sequences only what one SM would
+  // take longer for than the whole card for all
+  int64_t seg = (tiles + 4 * kSms - 1) / (4 * kSms);
+  if (d->n_seqs * groups >= 2 * kSms) seg = std::max(seg, tiles / 128);
+  seg = std::min<int64_t>(std::max<int64_t>(seg, 4), 1 << 20);
+  p.seg_tokens = (int)(seg * kPlTile);
+  p.extra = d->tokens / p.seg_tokens;
+  p.total = align_up((size_t)p.extra * d->heads * d->head_dim * d->head_dim * sizeof(float));
+  return p;
+}
+
+template <int D>
+sala_status run_linear(const sala_packed_linear_desc* d, const void* q, const void* k, const void* v,
+                       const void* gate, const float* lambda, const int32_t* cu, const int32_t* slots,
+                       const float* state_in, float* state_out, void* out, float* ws, cudaStream_t st) {
+  const LinearPlan p = linear_plan(d);
+  const int64_t groups = (d->heads + 128 / D - 1) / (128 / D);
+  CUtensorMap qm, km, vm;
+  const uint64_t cols = (uint64_t)d->heads * D;
+  if (!make_tmap_bf16(&qm, q, cols, d->tokens, 64, kPlTile) ||
+      !make_tmap_bf16(&km, k, cols, d->tokens, 64, kPlTile) ||
+      !make_tmap_bf16(&vm, v, cols, d->tokens, 64, kPlTile))
+    return SALA_ERR_CUDA;
+  const size_t smem = PlLayout::kBytes + 1024;
+  const int64_t units = (p.extra + d->n_seqs) * groups;
+  if (units > 0x7fffffffll) return SALA_ERR_UNSUPPORTED;
+  auto launch = [&](auto kern, int64_t grid) {
+    if (allow_smem(kern, smem) != cudaSuccess) return SALA_ERR_CUDA;
+    kern<<<(unsigned)grid, kPlThreads, smem, st>>>(
+        qm, km, vm, static_cast<const bf16*>(v), static_cast<const bf16*>(gate), lambda, cu, slots, state_in,
+        state_out, ws, static_cast<bf16*>(out), d->tokens, d->n_seqs, d->n_slots, d->heads, p.seg_tokens,
+        d->scale);
+    return launch_status();
+  };
+  if (p.extra > 0) {
+    sala_status s = launch(linear_packed_kernel<D, false>, p.extra * groups);
+    if (s != SALA_OK) return s;
+    const int64_t per = (int64_t)d->heads * D * D / 4;
+    const dim3 grid((unsigned)((per + kPlScanThreads - 1) / kPlScanThreads),
+                    (unsigned)std::min<int64_t>(d->n_seqs, p.extra));
+    if (grid.y > 65535) return SALA_ERR_UNSUPPORTED;
+    linear_packed_scan_kernel<D><<<grid, kPlScanThreads, 0, st>>>(
+        lambda, cu, slots, state_in, ws, d->tokens, d->n_seqs, d->n_slots, d->heads, p.seg_tokens);
+    s = launch_status();
+    if (s != SALA_OK) return s;
+  }
+  return launch(linear_packed_kernel<D, true>, units);
 }
 
 // How a decode step over a shared prefix is cut up.
@@ -264,8 +325,8 @@ sala_status sala_dense_prefill(const sala_dense_desc* d, const void* q_norm, con
 }
 
 size_t sala_linear_packed_workspace_size(const sala_packed_linear_desc* d) {
-  if (check_packed_linear(d) != SALA_OK) return 0;
-  return 0;
+  if (check_packed_linear(d) != SALA_OK || d->dtype != SALA_BF16) return 0;
+  return linear_plan(d).total;
 }
 
 sala_status sala_linear_packed_prefill(const sala_packed_linear_desc* d, const void* q_norm,
@@ -282,18 +343,14 @@ sala_status sala_linear_packed_prefill(const sala_packed_linear_desc* d, const v
       !aligned16_or_null(state_in) || !aligned16_or_null(state_out) || !aligned16(out))
     return SALA_ERR_INVALID_ARG;
   if (!slots && d->n_slots < d->n_seqs) return SALA_ERR_INVALID_ARG;
-  (void)workspace;
-  (void)ws_bytes;
+  const size_t need = linear_plan(d).total;
+  if (need > 0 && (!workspace || ws_bytes < need)) return SALA_ERR_WORKSPACE;
+  if (need > 0 && !aligned16(workspace)) return SALA_ERR_INVALID_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  auto launch = [&](auto kern, int D) {
-    kern<<<(unsigned)((long long)d->n_seqs * d->heads * (D / 32)), 256, 0, st>>>(
-        static_cast<const bf16*>(q_norm), static_cast<const bf16*>(k_norm),
-        static_cast<const bf16*>(v), static_cast<const bf16*>(gate), lambda, cu_seqlens, slots,
-        state_in, state_out, static_cast<bf16*>(out), d->tokens, d->heads, d->n_slots, d->scale);
-    return launch_status();
-  };
-  return d->head_dim == 128 ? launch(linear_packed_simt_kernel<128>, 128)
-                            : launch(linear_packed_simt_kernel<64>, 64);
+  float* ws = static_cast<float*>(workspace);
+  if (d->head_dim == 128)
+    return run_linear<128>(d, q_norm, k_norm, v, gate, lambda, cu_seqlens, slots, state_in, state_out, out, ws, st);
+  return run_linear<64>(d, q_norm, k_norm, v, gate, lambda, cu_seqlens, slots, state_in, state_out, out, ws, st);
 }
 
 sala_status sala_linear_packed_step(const sala_packed_linear_desc* d, const void* q_norm,

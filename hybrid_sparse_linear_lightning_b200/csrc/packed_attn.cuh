@@ -164,12 +164,11 @@ __device__ __forceinline__ void pa_run(const CUtensorMap& qmap, const CUtensorMa
   uint64_t* ring_empty = ring_full + L::kSlots;
   uint64_t* s_full = ring_empty + L::kSlots;   // [2]
   uint64_t* p_full = s_full + 2;               // [2]
-  // block fix_from + k is published on v_ready[k % 3]: the warps that go over
-  // V run at most two blocks ahead of the products (a third tile would have to
-  // enter the ring before the first has left it)
+  // block fix_from + k is published on v_ready[k]: two tiles hold at most 256
+  // tokens, so their diagonal crosses at most three blocks
   uint64_t* v_ready = p_full + 2;
-  // such a tile's load completes on fix_full[k % 3] (and only counts a phase of
-  // its ring barrier): every phase of these barriers has exactly one wait for it
+  // such a tile's load completes on fix_full[k] (and only counts a phase of its
+  // ring barrier): those who go over it have not followed the ring's phases
   uint64_t* fix_full = v_ready + 3;
   uint64_t* fin = fix_full + 3;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMisc);
@@ -224,7 +223,7 @@ __device__ __forceinline__ void pa_run(const CUtensorMap& qmap, const CUtensorMa
           uint64_t* full = ring_full + st;
           if ((m & 1) && (m >> 1) >= job.fix_from) {
             tc::mbar_arrive(full);
-            full = fix_full + ((m >> 1) - job.fix_from) % 3;
+            full = fix_full + ((m >> 1) - job.fix_from);
           }
           tc::mbar_expect_tx(full, L::kTile);
           uint8_t* dst = smem + L::kRing + st * L::kTile;
@@ -235,7 +234,7 @@ __device__ __forceinline__ void pa_run(const CUtensorMap& qmap, const CUtensorMa
         // no copy is in flight when this warp ends, whatever became of the others
         for (int i = max(0, m - L::kSlots); i < m; ++i) {
           const int k = (i >> 1) - job.fix_from;
-          if ((i & 1) && k >= 0) tc::mbar_wait(fix_full + k % 3, (k / 3) & 1);
+          if ((i & 1) && k >= 0) tc::mbar_wait(fix_full + k, 0);
           else tc::mbar_wait(ring_full + i % L::kSlots, (i / L::kSlots) & 1);
         }
       }
@@ -282,7 +281,7 @@ __device__ __forceinline__ void pa_run(const CUtensorMap& qmap, const CUtensorMa
           if (!(ok = wait_tile(2 * j + 1))) break;
           if (j >= job.fix_from) {
             const int k = j - job.fix_from;
-            if (!(ok = tc::mbar_wait(v_ready + k % 3, (k / 3) & 1))) break;
+            if (!(ok = tc::mbar_wait(v_ready + k, 0))) break;
           }
           for (int t = 0; ok && t < 2; ++t) {
             if (j >= job.nb[t]) continue;
@@ -304,12 +303,12 @@ __device__ __forceinline__ void pa_run(const CUtensorMap& qmap, const CUtensorMa
       bool bad = false;
       for (int j = job.fix_from; j < nb; ++j) {
         const int m = 2 * j + 1, k = j - job.fix_from;
-        if (!__all_sync(0xffffffffu, tc::mbar_wait(fix_full + k % 3, (k / 3) & 1))) break;
+        if (!__all_sync(0xffffffffu, tc::mbar_wait(fix_full + k, 0))) break;
         bad |= scrub_v<D>(smem + L::kRing + (m % L::kSlots) * L::kTile, job.n_keys - j * kPaBlock,
                           threadIdx.x - 64);
         tc::fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(v_ready + k % 3);
+        if (lane == 0) tc::mbar_arrive(v_ready + k);
       }
       if (bad) *found = 1;
       __threadfence_block();

@@ -330,4 +330,20 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, bool a_mn_ma
 }
 
 }  // namespace tc
+
+// 32 fp32 values -> bf16 columns [32 j, 32 j + 32) of row r of a [128 x 128]
+// bf16 tile stored as two 128-byte-swizzled column atoms of 64.
+__device__ __forceinline__ void sw128_store_row32(uint8_t* tile, int r, int j, const float* v) {
+  uint8_t* atom = tile + (j >> 1) * 16384 + r * 128;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int ch = (j & 1) * 4 + q;
+    uint4 u;
+    __nv_bfloat162* h2 = reinterpret_cast<__nv_bfloat162*>(&u);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) h2[e] = __floats2bfloat162_rn(v[q * 8 + 2 * e], v[q * 8 + 2 * e + 1]);
+    *reinterpret_cast<uint4*>(atom + ((ch ^ (r & 7)) << 4)) = u;
+  }
+}
+
 }  // namespace sala
