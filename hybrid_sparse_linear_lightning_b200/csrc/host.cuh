@@ -35,6 +35,20 @@ inline cudaError_t allow_smem(K kernel, size_t bytes) {
   return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
 }
 
+// The same, asked of the driver once per kernel and device: for kernels whose
+// `bytes` never change.
+template <typename K>
+inline cudaError_t allow_smem_once(K kernel, size_t bytes, std::atomic<uint64_t>* done) {
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (done->load(std::memory_order_acquire) & bit) return cudaSuccess;
+  const cudaError_t r = allow_smem(kernel, bytes);
+  if (r == cudaSuccess) done->fetch_or(bit, std::memory_order_release);
+  return r;
+}
+
 // base^(-2i/D) for i < D/2 in fp64
 inline RopeFreq rope_freq(int D, float base) {
   RopeFreq rf;

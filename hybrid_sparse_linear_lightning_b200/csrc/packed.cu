@@ -83,10 +83,16 @@ sala_status run_qk_norm(const sala_qk_norm_desc* d, const void* q, const void* k
                         const float* wk, const int32_t* pos, void* qn, void* kn, cudaStream_t st) {
   // several tokens per CTA only where there are CTAs enough to fill the card
   const int tpc = d->tokens >= 2048 ? kQkNormMaxTokens : 1;
+  // the last frequency table stays: forming one takes longer than a small launch
+  static thread_local float base = 0.f;
+  static thread_local RopeFreq freq;
+  if (pos && base != d->rope_base) {
+    freq = rope_freq(D, d->rope_base);
+    base = d->rope_base;
+  }
   qk_norm_kernel<T, D><<<(d->tokens + tpc - 1) / tpc, kQkNormThreads, 0, st>>>(
       static_cast<const T*>(q), static_cast<const T*>(k), wq, wk, pos, static_cast<bf16*>(qn),
-      static_cast<bf16*>(kn), d->tokens, tpc, d->q_heads, d->k_heads, rope_freq(D, d->rope_base),
-      d->rms_eps);
+      static_cast<bf16*>(kn), d->tokens, tpc, d->q_heads, d->k_heads, freq, d->rms_eps);
   return launch_status();
 }
 
@@ -118,7 +124,8 @@ sala_status run_dense(const sala_dense_desc* d, const void* q, const void* k, co
     return SALA_ERR_CUDA;
   auto kern = dense_attn_kernel<D>;
   const size_t smem = PaLayout<D>::kBytes + 1024;
-  if (allow_smem(kern, smem) != cudaSuccess) return SALA_ERR_CUDA;
+  static std::atomic<uint64_t> allowed{0};
+  if (allow_smem_once(kern, smem, &allowed) != cudaSuccess) return SALA_ERR_CUDA;
   // every sequence ends in a pair of tiles that may be part empty
   const int64_t pairs = (int64_t)d->tokens / (2 * Tt) + d->n_seqs;
   if (pairs * d->kv_heads > 0x7fffffffll) return SALA_ERR_UNSUPPORTED;
@@ -166,8 +173,9 @@ sala_status run_linear(const sala_packed_linear_desc* d, const void* q, const vo
   const size_t smem = PlLayout::kBytes + 1024;
   const int64_t units = (p.extra + d->n_seqs) * groups;
   if (units > 0x7fffffffll) return SALA_ERR_UNSUPPORTED;
-  auto launch = [&](auto kern, int64_t grid) {
-    if (allow_smem(kern, smem) != cudaSuccess) return SALA_ERR_CUDA;
+  static std::atomic<uint64_t> allowed[2];
+  auto launch = [&](auto kern, int64_t grid, std::atomic<uint64_t>* done) {
+    if (allow_smem_once(kern, smem, done) != cudaSuccess) return SALA_ERR_CUDA;
     kern<<<(unsigned)grid, kPlThreads, smem, st>>>(
         qm, km, vm, static_cast<const bf16*>(v), static_cast<const bf16*>(gate), lambda, cu, slots, state_in,
         state_out, ws, static_cast<bf16*>(out), d->tokens, d->n_seqs, d->n_slots, d->heads, p.seg_tokens,
@@ -175,7 +183,7 @@ sala_status run_linear(const sala_packed_linear_desc* d, const void* q, const vo
     return launch_status();
   };
   if (p.extra > 0) {
-    sala_status s = launch(linear_packed_kernel<D, false>, p.extra * groups);
+    sala_status s = launch(linear_packed_kernel<D, false>, p.extra * groups, &allowed[0]);
     if (s != SALA_OK) return s;
     const int64_t per = (int64_t)d->heads * D * D / 4;
     const dim3 grid((unsigned)((per + kPlScanThreads - 1) / kPlScanThreads),
@@ -186,7 +194,7 @@ sala_status run_linear(const sala_packed_linear_desc* d, const void* q, const vo
     s = launch_status();
     if (s != SALA_OK) return s;
   }
-  return launch(linear_packed_kernel<D, true>, units);
+  return launch(linear_packed_kernel<D, true>, units, &allowed[1]);
 }
 
 // How a decode step over a shared prefix is cut up.
@@ -243,7 +251,8 @@ sala_status run_prefix(const sala_prefix_desc* d, const void* q, const void* k, 
         !make_tmap_bf16(&vm, pv, kv_cols, d->prefix_len, 64, kPaBlock))
       return SALA_ERR_CUDA;
     const size_t smem = PaLayout<D>::kBytes + 1024;
-    if (allow_smem(prefix_attn_kernel<D>, smem) != cudaSuccess) return SALA_ERR_CUDA;
+    static std::atomic<uint64_t> allowed{0};
+    if (allow_smem_once(prefix_attn_kernel<D>, smem, &allowed) != cudaSuccess) return SALA_ERR_CUDA;
     const int64_t units = (int64_t)p.n_split * p.pairs * d->kv_heads;
     prefix_attn_kernel<D><<<(unsigned)units, kPaThreads, smem, st>>>(
         qm, km, vm, part_o, part_ml, d->batch, d->q_heads, d->kv_heads, p.Tt, p.pairs, d->prefix_len,
@@ -260,7 +269,8 @@ sala_status run_prefix(const sala_prefix_desc* d, const void* q, const void* k, 
   if (units * cs > 0x7fffffffll) return SALA_ERR_UNSUPPORTED;
   auto kern = own_attn_kernel<D>;
   const size_t smem = OwnLayout<D>::kBytes;
-  if (allow_smem(kern, smem) != cudaSuccess) return SALA_ERR_CUDA;
+  static std::atomic<uint64_t> allowed{0};
+  if (allow_smem_once(kern, smem, &allowed) != cudaSuccess) return SALA_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(units * cs));
   cfg.blockDim = dim3(32 * kOwnWarps);

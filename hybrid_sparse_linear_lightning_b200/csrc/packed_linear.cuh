@@ -41,10 +41,11 @@ namespace sala {
 
 constexpr int kPlThreads = 512;
 constexpr int kPlTile = 128;
-// warpgroup 0: TMA, MMA, TMEM; 1: V; 2: P and outputs; 3: state.  The shares sum
-// to the 4 x 128 registers that the block is launched with (warpgroup 2 keeps its own).
-constexpr int kPlRegs0 = 48, kPlRegs1 = 152, kPlRegs2 = 128, kPlRegs3 = 184;
-static_assert(kPlRegs0 + kPlRegs1 + kPlRegs2 + kPlRegs3 <= 4 * 128, "register split exceeds the launch");
+// warpgroup 0: TMA, MMA, TMEM; 1 and 3: V and the state, half the columns each;
+// 2: P and outputs.  The shares sum to the 4 x 128 registers that the block is
+// launched with.
+constexpr int kPlRegs0 = 56, kPlRegsV = 152, kPlRegs2 = 152;
+static_assert(kPlRegs0 + 2 * kPlRegsV + kPlRegs2 <= 4 * 128, "register split exceeds the launch");
 
 struct PlLayout {
   static constexpr int kQ = 0, kK = 32768, kV = 65536;     // per stage, two 64-column atoms each
@@ -55,11 +56,22 @@ struct PlLayout {
   // ld_full[2], ld_empty[2], kv_ok, qk_full, p_full, pv_done, o_full, o_empty, s_full, v_hi, v_lo,
   // hi_done, ds_full[2], fin
   static constexpr int kNumBars = 17;
-  static constexpr int kMisc = kBar + 8 * kNumBars;        // TMEM address, unit, found[2][4]
-  static constexpr int kBytes = kMisc + 96;
+  static constexpr int kMisc = kBar + 8 * kNumBars;        // TMEM address, unit, found[2][8]
+  static constexpr int kBytes = kMisc + 128;
   static constexpr int kColQK = 0, kColO1 = 128, kColO2 = 256, kColDs = 384;
   static_assert(kBar % 8 == 0 && kMisc % 8 == 0, "alignment");
 };
+
+// lam^n by squaring in fp64 (n >= 0): no call of a library function, across
+// which the kernel's values would have to be kept in memory.
+__device__ __forceinline__ float decay_pow(float lam, int n) {
+  double p = 1.0, b = lam;
+  for (; n > 0; n >>= 1) {
+    if (n & 1) p *= b;
+    b *= b;
+  }
+  return (float)p;
+}
 
 // How a call's sequences are cut: segments of seg_tokens.  What a CTA finds
 // for its index p among the sequences' segments (all of them, or all but each
@@ -105,6 +117,43 @@ __device__ __forceinline__ PlUnit find_segment(const int32_t* cu, int n_seqs, in
   return PlUnit{-1, 0, 0, 0};
 }
 
+// A load that stays where it is written: the compiler would else move it to
+// its first use, behind the wait that is to cover its latency.
+__device__ __forceinline__ uint4 ld_now(const __nv_bfloat16* p) {
+  uint4 u;
+  asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "l"(p));
+  return u;
+}
+
+// 16 bytes of shared memory by its 32-bit address.
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+  uint4 u;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "r"(a) : "memory");
+  return u;
+}
+__device__ __forceinline__ void sts16(uint32_t a, const uint4& u) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(u.x), "r"(u.y), "r"(u.z), "r"(u.w) : "memory");
+}
+
+// sigmoid(g) o for eight values: o / (1 + 2^(-g log2 e)), rounded to bf16.
+__device__ __forceinline__ uint4 gate_pack(const uint4& g, const uint4& a, const uint4& b) {
+  const uint32_t gw[4] = {g.x, g.y, g.z, g.w}, ow[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  uint32_t r[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    constexpr float kL = -1.4426950408889634f;
+    const float2 z = __fmul2_rn(__bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&gw[e])), make_float2(kL, kL));
+    const float2 d = __fadd2_rn(make_float2(tc::ex2_approx(z.x), tc::ex2_approx(z.y)), make_float2(1.f, 1.f));
+    float2 q;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q.x) : "f"(d.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q.y) : "f"(d.y));
+    q = __fmul2_rn(q, make_float2(__uint_as_float(ow[2 * e]), __uint_as_float(ow[2 * e + 1])));
+    const __nv_bfloat162 h2 = __floats2bfloat162_rn(q.x, q.y);
+    r[e] = *reinterpret_cast<const uint32_t*>(&h2);
+  }
+  return make_uint4(r[0], r[1], r[2], r[3]);
+}
+
 // bf16 pair (w) times (f, f): high and low bf16 parts.
 __device__ __forceinline__ void split_pair(uint32_t w, float f, uint32_t* hi, uint32_t* lo) {
   const float2 x = __fmul2_rn(__bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w)), make_float2(f, f));
@@ -131,7 +180,7 @@ linear_packed_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBar);
   // Every barrier's phase is waited for by all who wait on it before the next
   // one can complete.  Where kOut is false, tiles of even and odd number use
-  // kv_ok / v_hi (V' written) and o_empty / s_full (sum read) in turn for that.
+  // kv_ok and v_hi (V' written) in turn for that.
   uint64_t* ld_full = bars;            // [2] Q, K, V of a tile have landed
   uint64_t* ld_empty = bars + 2;       // [2]
   uint64_t* kv_ok = bars + 4;          // rows past the end and non-finite values are 0
@@ -148,7 +197,7 @@ linear_packed_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
   uint64_t* fin = bars + 16;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMisc);
   PlUnit* unit = reinterpret_cast<PlUnit*>(smem + L::kMisc + 8);
-  volatile int* found = reinterpret_cast<volatile int*>(smem + L::kMisc + 32);   // [2][4]
+  volatile int* found = reinterpret_cast<volatile int*>(smem + L::kMisc + 32);   // [2][8]
   float* pw = reinterpret_cast<float*>(smem + L::kPw);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -198,26 +247,25 @@ linear_packed_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(ld_full + i, 1);
-      tc::mbar_init(ld_empty + i, 1);
+      tc::mbar_init(ld_empty + i, kOut ? 2 : 1);     // products done, and outputs written
       tc::mbar_init(ds_full + i, 1);
     }
-    tc::mbar_init(kv_ok, 4);
+    tc::mbar_init(kv_ok, 8);
     tc::mbar_init(qk_full, 1);
     tc::mbar_init(p_full, 4);
     tc::mbar_init(pv_done, 1);
     tc::mbar_init(o_full, 1);
     tc::mbar_init(o_empty, 4);
-    tc::mbar_init(s_full, 4);
-    tc::mbar_init(v_hi, 4);
-    tc::mbar_init(v_lo, 4);
+    tc::mbar_init(s_full, 8);
+    tc::mbar_init(v_hi, 8);
+    tc::mbar_init(v_lo, 8);
     tc::mbar_init(hi_done, 1);
     tc::mbar_init(fin, 1);
     tc::fence_barrier_init();
   }
   for (int e = threadIdx.x; e < NH * 129; e += kPlThreads) {
     const int hh = e / 129, x = e % 129;
-    const double lam = hg * NH + hh < H ? (double)lambda[hg * NH + hh] : 0.0;
-    pw[hh * 132 + x] = (float)pow(lam, (double)x);
+    pw[hh * 132 + x] = hg * NH + hh < H ? decay_pow(lambda[hg * NH + hh], x) : 0.f;
   }
   if (warp == 2) {
     tc::tmem_alloc(tmem_slot, 512);
@@ -341,8 +389,7 @@ linear_packed_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
           for (int c = 0; ok && c < nt; ++c) {
             const int x = c & 1, use = c >> 1;
             if (!(ok = tc::mbar_wait(ld_full + x, use & 1) && tc::mbar_wait(x ? v_hi : kv_ok, use & 1))) break;
-            // the buffer's last sum has been read
-            if (use > 0 && !(ok = tc::mbar_wait(x ? s_full : o_empty, (use - 1) & 1))) break;
+            // (who wrote V' of this tile has read the sum of tile c - 2 before)
             tc::tc_fence_after();
             issue_ds(c, L::kV, L::kColDs - 128 * (c & 1), false);
             issue_ds(c, L::kQ, L::kColDs - 128 * (c & 1), true);
@@ -354,137 +401,17 @@ linear_packed_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
         tc::mbar_wait(fin, 0);
       }
     }
-  } else if (warp < 8) {
-    // ---------------------------------------------------------------- V
-    tc::setmaxnreg_inc<kPlRegs1>();
-    const int r = r_own;                      // token row of the tile
-    auto chunk = [&](uint8_t* tile, int i) {  // 16-byte chunk i (of 16) of this row
-      return reinterpret_cast<uint4*>(tile + (i >> 3) * 16384 + r * 128 + (((i & 7) ^ (r & 7)) << 4));
-    };
-    uint4 raw[16];
-    // reads the row into registers and makes the tile safe to multiply
-    auto enter = [&](int c) {
-      if (!__all_sync(0xffffffffu, tc::mbar_wait(ld_full + (c & 1), (c >> 1) & 1))) return false;
-      uint8_t* stage = smem + (c & 1) * L::kStage;
-      if (r < tile_len(c)) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) raw[i] = *chunk(stage + L::kV, i);
-      } else {
-        const uint4 z = make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          raw[i] = z;
-          *chunk(stage + L::kV, i) = z;
-          *chunk(stage + L::kK, i) = z;
-        }
-      }
-      return true;
-    };
-    bool ok = enter(0);
-    if constexpr (kOut) {
-      uint4 lo[16];
-      // before P V: non-finite values become 0 in the tile
-      auto make_safe = [&](int c) {
-        uint32_t acc = 0;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          acc |= (raw[i].x & 0x7f807f80u) + 0x00800080u;
-          acc |= (raw[i].y & 0x7f807f80u) + 0x00800080u;
-          acc |= (raw[i].z & 0x7f807f80u) + 0x00800080u;
-          acc |= (raw[i].w & 0x7f807f80u) + 0x00800080u;
-        }
-        const bool bad = (acc & 0x80008000u) != 0;
-        if (bad) {
-#pragma unroll 1
-          for (int i = 0; i < 16; ++i) {
-            uint4* p = chunk(smem + (c & 1) * L::kStage + L::kV, i);
-            const uint4 x = *p;
-            const unsigned m = nonfinite8(x);
-            uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              if (m >> (2 * e) & 1) w[e] &= 0xffff0000u;
-              if (m >> (2 * e + 1) & 1) w[e] &= 0xffffu;
-            }
-            *p = make_uint4(w[0], w[1], w[2], w[3]);
-          }
-        }
-        const bool any = __any_sync(0xffffffffu, bad);
-        if (lane == 0) found[(c & 1) * 4 + (warp & 3)] = any;
-        tc::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(kv_ok);
-      };
-      if (ok) make_safe(0);
-      for (int c = 0; ok && c < nt; ++c) {
-        const bool want = c < nds;
-        if (!(ok = __all_sync(0xffffffffu, tc::mbar_wait(pv_done, c & 1)))) break;
-        if (want) {
-          const int Lt = tile_len(c);
-          uint8_t* tile = smem + (c & 1) * L::kStage + L::kV;
-          const float f0 = r < Lt ? pw[Lt - 1 - r] : 0.f;
-          const float f1 = NH == 1 ? f0 : (r < Lt ? pw[132 + Lt - 1 - r] : 0.f);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            uint4 hi;
-            const float f = i < 8 ? f0 : f1;
-            split_pair(raw[i].x, f, &hi.x, &lo[i].x);
-            split_pair(raw[i].y, f, &hi.y, &lo[i].y);
-            split_pair(raw[i].z, f, &hi.z, &lo[i].z);
-            split_pair(raw[i].w, f, &hi.w, &lo[i].w);
-            *chunk(tile, i) = hi;
-          }
-          tc::fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive(v_hi);
-        }
-        if (c + 1 < nt) {
-          if (!(ok = enter(c + 1))) break;
-          make_safe(c + 1);
-        }
-        if (want) {
-          if (!(ok = __all_sync(0xffffffffu, tc::mbar_wait(hi_done, c & 1)))) break;
-          uint8_t* tile = smem + (c & 1) * L::kStage + L::kV;
-#pragma unroll
-          for (int i = 0; i < 16; ++i) *chunk(tile, i) = lo[i];
-          tc::fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive(v_lo);
-        }
-      }
-    } else {
-      for (int c = 0; ok && c < nt; ++c) {
-        const int Lt = tile_len(c);
-        uint8_t* stage = smem + (c & 1) * L::kStage;
-        const float f0 = r < Lt ? pw[Lt - 1 - r] : 0.f;
-        const float f1 = NH == 1 ? f0 : (r < Lt ? pw[132 + Lt - 1 - r] : 0.f);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          uint4 hi, lo;
-          const float f = i < 8 ? f0 : f1;
-          split_pair(raw[i].x, f, &hi.x, &lo.x);
-          split_pair(raw[i].y, f, &hi.y, &lo.y);
-          split_pair(raw[i].z, f, &hi.z, &lo.z);
-          split_pair(raw[i].w, f, &hi.w, &lo.w);
-          *chunk(stage + L::kV, i) = hi;
-          *chunk(stage + L::kQ, i) = lo;
-        }
-        tc::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(c & 1 ? v_hi : kv_ok);
-        if (c + 1 < nt) ok = enter(c + 1);
-      }
-    }
-  } else if (warp < 12) {
+  } else if (warp >= 8 && warp < 12) {
     // ------------------------------------------------------- P and gated outputs
+    tc::setmaxnreg_inc<kPlRegs2>();
     if constexpr (kOut) {
       const int quad = warp & 3, r = r_own;      // token row
       const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
       const int cols = min(128, H * D - hg * 128);      // columns of heads that exist
       for (int c = 0; c < nt; ++c) {
         if (!__all_sync(0xffffffffu, tc::mbar_wait(kv_ok, c & 1))) break;
-        const volatile int* fc = found + (c & 1) * 4;
-        const bool bad = fc[0] | fc[1] | fc[2] | fc[3];
+        const volatile int* fc = found + (c & 1) * 8;
+        const bool bad = fc[0] | fc[1] | fc[2] | fc[3] | fc[4] | fc[5] | fc[6] | fc[7];
         bool ok = true;
 #pragma unroll 1
         for (int hs = 0; hs < NH; ++hs) {
@@ -504,16 +431,23 @@ linear_packed_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
 #pragma unroll
                 for (int e = 0; e < 32; ++e) xv[e] = e <= lane ? xv[e] * pwh[lane - e] : 0.f;
               } else {
-                const int a = r - 32 * q0;            // element e decays by lam^(a - e)
-                float2 dcy = make_float2(pwh[a - 30], pwh[a - 31]);
-                const float2 l2 = make_float2(pwh[2], pwh[2]);
+                // element e decays by lam^(a - e): four pairs with powers of their own,
+                // lam^8 from one to the next, from the largest power down
+                const int a = r - 32 * q0;
+                float2 dcy[4];
 #pragma unroll
-                for (int e = 30; e >= 0; e -= 2) {
-                  const float2 y = __fmul2_rn(make_float2(xv[e], xv[e + 1]), dcy);
-                  xv[e] = y.x;
-                  xv[e + 1] = y.y;
-                  dcy = __fmul2_rn(dcy, l2);
-                }
+                for (int x = 0; x < 4; ++x) dcy[x] = make_float2(pwh[a - 24 - 2 * x], pwh[a - 25 - 2 * x]);
+                const float2 l8 = make_float2(pwh[8], pwh[8]);
+#pragma unroll
+                for (int e0 = 24; e0 >= 0; e0 -= 8)
+#pragma unroll
+                  for (int x = 0; x < 4; ++x) {
+                    const int e = e0 + 2 * x;
+                    const float2 y = __fmul2_rn(make_float2(xv[e], xv[e + 1]), dcy[x]);
+                    xv[e] = y.x;
+                    xv[e + 1] = y.y;
+                    dcy[x] = __fmul2_rn(dcy[x], l8);
+                  }
               }
 #pragma unroll
               for (int e = 0; e < 16; ++e) {
@@ -533,86 +467,178 @@ linear_packed_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
         }
         if (!ok) break;
         // ---- out = sigmoid(gate) scale (lam^(r+1) O1 + O2)
-        const bool valid = r < tile_len(c);
-        const long long row = ((long long)(s0 + c * kPlTile + r) * H) * D + hg * 128;
-        uint4 g[16];
-        if (valid) {
+        // A thread holds a token's row, whose neighbours lie H d values apart:
+        // 64 columns at a time go through the tile's Q, which no product needs any
+        // more, so that gate and out are read and written 128 bytes a row.
+        const int Lt = tile_len(c);
+        const int cr = quad * 4 + (lane >> 3), cq = lane & 7;      // row (+ 16 i) and 8-column chunk
+        const long long at = (long long)(s0 + c * kPlTile + cr) * H * D + hg * 128 + 8 * cq;
+        uint4 g[8];
+        auto load_gate = [&](int h) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (8 * i < cols) g[i] = *reinterpret_cast<const uint4*>(gate + row + 8 * i);
-        }
+          for (int i = 0; i < 8; ++i)
+            if (cr + 16 * i < Lt && 64 * h < cols) g[i] = ld_now(gate + at + (long long)i * 16 * H * D + 64 * h);
+        };
+        load_gate(0);
         if (!__all_sync(0xffffffffu, tc::mbar_wait(o_full, c & 1))) break;
         tc::tc_fence_after();
+        // 16-byte chunk x of a row of 64 fp32: free of bank conflicts by rows and by columns
+        const uint32_t stg = tc::smem_u32(smem) + (c & 1) * L::kStage + L::kQ;
+        auto stage_at = [&](int row, int x) {
+          return (stg + row * 256 + ((row & 7) << 4)) ^ (((x >> 1) | ((x & 1) << 3)) << 4);
+        };
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {                   // 16 columns at a time
-          float o1[16], o2[16];
-          tc::tmem_ld16(lane_base + L::kColO1 + 16 * j, o1);
-          tc::tmem_ld16(lane_base + L::kColO2 + 16 * j, o2);
-          tc::tmem_wait_ld();
-          if (j == 7) {
-            tc::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(o_empty);
-          }
-          const float f = pw[(16 * j / D) * 132 + r + 1];
+        for (int h = 0; h < 2; ++h) {
+          const float f = scale * pw[(64 * h / D) * 132 + r + 1];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) o1[e] = fmaf(f, o1[e], o2[e]);
-          if (bad && valid && 16 * j < cols) {
-            for (int t = 0; t <= r; ++t) {
-              const __nv_bfloat16* vr = v + (long long)(s0 + c * kPlTile + t) * H * D + hg * 128 + 16 * j;
+          for (int j = 0; j < 2; ++j) {                 // 32 columns at a time
+            float o1[32], o2[32];
+            tc::tmem_ld32(lane_base + L::kColO1 + 64 * h + 32 * j, o1);
+            tc::tmem_ld32(lane_base + L::kColO2 + 64 * h + 32 * j, o2);
+            tc::tmem_wait_ld();
+            if (h == 1 && j == 1) {
+              tc::tc_fence_before();
+              __syncwarp();
+              if (lane == 0) tc::mbar_arrive(o_empty);
+            }
 #pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                const float x = to_f32(vr[e]);
-                if (!isfinite(x)) o1[e] += x;
+            for (int e = 0; e < 32; e += 2) {
+              const float2 y = __ffma2_rn(make_float2(f, f), make_float2(o1[e], o1[e + 1]),
+                                          __fmul2_rn(make_float2(scale, scale), make_float2(o2[e], o2[e + 1])));
+              o1[e] = y.x;
+              o1[e + 1] = y.y;
+            }
+            if (bad && r < Lt && 64 * h < cols) {
+              for (int t = 0; t <= r; ++t) {
+                const __nv_bfloat16* vr = v + (long long)(s0 + c * kPlTile + t) * H * D + hg * 128 + 64 * h + 32 * j;
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                  const float x = to_f32(vr[e]);
+                  if (!isfinite(x)) o1[e] += x;
+                }
               }
             }
-          }
-          if (valid && 16 * j < cols) {
 #pragma unroll
-            for (int e = 0; e < 16; e += 8) {
-              float gv[8];
-              load8(reinterpret_cast<const __nv_bfloat16*>(&g[2 * j + e / 8]), gv);
-#pragma unroll
-              for (int x = 0; x < 8; ++x) gv[x] = sigmoidf_(gv[x]) * (scale * o1[e + x]);
-              store8(out + row + 16 * j + e, gv);
-            }
+            for (int x = 0; x < 8; ++x)
+              sts16(stage_at(r, 8 * j + x),
+                    make_uint4(__float_as_uint(o1[4 * x]), __float_as_uint(o1[4 * x + 1]),
+                               __float_as_uint(o1[4 * x + 2]), __float_as_uint(o1[4 * x + 3])));
           }
+          tc::named_sync(2, 128);
+          // all loads first: each thread's eight rows then overlap
+          uint4 a[8], b[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            a[i] = lds16(stage_at(cr + 16 * i, 2 * cq));
+            b[i] = lds16(stage_at(cr + 16 * i, 2 * cq + 1));
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) a[i] = gate_pack(g[i], a[i], b[i]);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (cr + 16 * i < Lt && 64 * h < cols)
+              *reinterpret_cast<uint4*>(out + at + (long long)i * 16 * H * D + 64 * h) = a[i];
+          if (h == 0) load_gate(1);
+          if (h == 1) tc::fence_proxy_async_smem();      // the next load writes there
+          tc::named_sync(2, 128);
         }
+        if (threadIdx.x == 256) tc::mbar_arrive(ld_empty + (c & 1));
       }
     }
   } else {
-    // ---------------------------------------------------------------- state
-    tc::setmaxnreg_inc<kPlRegs3>();
-    const int quad = warp & 3, r = r_own;      // key row of S (of head hsub)
-    const uint32_t ds_addr = tmem + ((uint32_t)(quad * 32) << 16) + L::kColDs + hsub * D % 128;
-    const float* pwh = pw + hsub * 132;
-    float S[D];
+    // --------------------------------------------- V and the state (half the columns each)
+    tc::setmaxnreg_inc<kPlRegsV>();
+    const int quad = warp & 3, half = warp >= 12;
+    const int r = r_own;                      // token row of V, key row of S (of head hsub)
+    // 16-byte chunk i (of 8) of this half row of the tile at offset `part` of stage c & 1
+    const uint32_t row_a = tc::smem_u32(smem) + half * 16384 + r * 128 + ((r & 7) << 4);
+    auto chunk = [&](int c, int part, int i) { return (row_a + (c & 1) * L::kStage + part) ^ (i << 4); };
+    // makes the tile safe to multiply; says whether this part of V held values
+    // that are not finite (they are 0 now).  False where a wait ran out.
+    auto enter = [&](int c, bool* bad) {
+      if (!__all_sync(0xffffffffu, tc::mbar_wait(ld_full + (c & 1), (c >> 1) & 1))) return false;
+      *bad = false;
+      if (r >= tile_len(c)) {
 #pragma unroll
-    for (int e = 0; e < D; e += 4) {
-      const float4 x = s_src ? __ldcg(reinterpret_cast<const float4*>(s_src + e)) : make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i = 0; i < 8; ++i) {
+          sts16(chunk(c, L::kV, i), make_uint4(0, 0, 0, 0));
+          sts16(chunk(c, L::kK, i), make_uint4(0, 0, 0, 0));
+        }
+      } else if (kOut) {
+        uint32_t acc = 0;
+        uint4 x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = lds16(chunk(c, L::kV, i));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {      // an exponent of ones carries into bit 15 of its half
+          acc |= ((x[i].x & 0x7f807f80u) + 0x00800080u) | ((x[i].y & 0x7f807f80u) + 0x00800080u);
+          acc |= ((x[i].z & 0x7f807f80u) + 0x00800080u) | ((x[i].w & 0x7f807f80u) + 0x00800080u);
+        }
+        *bad = (acc & 0x80008000u) != 0;
+        if (*bad) {
+#pragma unroll 1
+          for (int i = 0; i < 8; ++i) {
+            const uint4 x = lds16(chunk(c, L::kV, i));
+            const unsigned m = nonfinite8(x);
+            uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              if (m >> (2 * e) & 1) w[e] &= 0xffff0000u;
+              if (m >> (2 * e + 1) & 1) w[e] &= 0xffffu;
+            }
+            sts16(chunk(c, L::kV, i), make_uint4(w[0], w[1], w[2], w[3]));
+          }
+        }
+      }
+      if (kOut) {
+        const bool any = __any_sync(0xffffffffu, *bad);
+        if (lane == 0) found[(c & 1) * 8 + half * 4 + quad] = any;
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(kv_ok);
+      }
+      return true;
+    };
+    const float* pwv = pw + (NH == 1 ? 0 : half) * 132;     // decays of the half's head
+    // the state: columns [64 half, 64 half + 64) of row r; where two heads lie
+    // side by side only the half of the row's own head
+    const bool mine = NH == 1 || half == hsub;
+    const uint32_t ds_addr = tmem + ((uint32_t)(quad * 32) << 16) + L::kColDs + 64 * half;
+    const int sc = NH == 1 ? 64 * half : 0;                 // first column within the head
+    float S[64];
+#pragma unroll
+    for (int e = 0; e < 64; e += 4) {
+      const float4 x = mine && s_src ? __ldcg(reinterpret_cast<const float4*>(s_src + sc + e))
+                                     : make_float4(0.f, 0.f, 0.f, 0.f);
       S[e] = x.x;
       S[e + 1] = x.y;
       S[e + 2] = x.z;
       S[e + 3] = x.w;
     }
     auto publish = [&]() {
+      if (mine) {
 #pragma unroll
-      for (int j = 0; j < D / 32; ++j) sw128_store_row32(smem + L::kS, r, hsub * (D / 32) + j, S + 32 * j);
+        for (int i = 0; i < 8; ++i) {
+          uint32_t w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const __nv_bfloat162 h2 = __floats2bfloat162_rn(S[8 * i + 2 * e], S[8 * i + 2 * e + 1]);
+            w[e] = *reinterpret_cast<const uint32_t*>(&h2);
+          }
+          sts16(chunk(0, L::kS, i), make_uint4(w[0], w[1], w[2], w[3]));
+        }
+      }
       tc::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(s_full);
     };
-    if (kOut) publish();
-    bool ok = true;
-    for (int c = 0; ok && c < nds; ++c) {
-      // ds_full of tile c says that Q S of tile c has read the copy of S as well
-      uint64_t* full = kOut ? ds_full : ds_full + (c & 1);
-      if (!(ok = __all_sync(0xffffffffu, tc::mbar_wait(full, kOut ? c & 1 : (c >> 1) & 1)))) break;
+    // S <- lam^L S + K^T V' of tile c
+    auto join = [&](int c, uint64_t* full, int parity, uint32_t src) {
+      if (!__all_sync(0xffffffffu, tc::mbar_wait(full, parity))) return false;
       tc::tc_fence_after();
-      const float f = pwh[tile_len(c)];
-      const uint32_t src = ds_addr - (kOut ? 0 : 128 * (c & 1));
+      const float f = pw[hsub * 132 + tile_len(c)];
 #pragma unroll
-      for (int j = 0; j < D / 16; ++j) {
+      for (int j = 0; j < 4; ++j) {
         float x[16];
         tc::tmem_ld16(src + 16 * j, x);
         tc::tmem_wait_ld();
@@ -620,17 +646,82 @@ linear_packed_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
         for (int e = 0; e < 16; ++e) S[16 * j + e] = fmaf(f, S[16 * j + e], x[e]);
       }
       tc::tc_fence_before();
+      return true;
+    };
+    bool bad = false, bad_next = false;
+    if (kOut) publish();
+    bool ok = enter(0, &bad);
+    for (int c = 0; ok && c < nt; ++c) {
+      const int Lt = tile_len(c);
       if constexpr (kOut) {
-        if (c + 1 < nt) publish();
+        const bool want = c < nds;
+        if (!(ok = __all_sync(0xffffffffu, tc::mbar_wait(pv_done, c & 1)))) break;
+        uint4 lo[8];
+        if (want) {
+          const float f = r < Lt ? pwv[Lt - 1 - r] : 0.f;
+          if (bad) {         // the state takes the row as it came
+            const __nv_bfloat16* vr = v + (long long)(s0 + c * kPlTile + r) * H * D + hg * 128 + 64 * half;
+#pragma unroll 1
+            for (int i = 0; i < 8; ++i) sts16(chunk(c, L::kV, i), *reinterpret_cast<const uint4*>(vr + 8 * i));
+          }
+          uint4 x[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[i] = lds16(chunk(c, L::kV, i));
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            uint4 hi;
+            split_pair(x[i].x, f, &hi.x, &lo[i].x);
+            split_pair(x[i].y, f, &hi.y, &lo[i].y);
+            split_pair(x[i].z, f, &hi.z, &lo[i].z);
+            split_pair(x[i].w, f, &hi.w, &lo[i].w);
+            x[i] = hi;
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) sts16(chunk(c, L::kV, i), x[i]);
+          tc::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(v_hi);
+        }
+        if (c + 1 < nt && !(ok = enter(c + 1, &bad_next))) break;
+        if (want) {
+          if (!(ok = __all_sync(0xffffffffu, tc::mbar_wait(hi_done, c & 1)))) break;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) sts16(chunk(c, L::kV, i), lo[i]);
+          tc::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(v_lo);
+          // the products being done says that Q S of this tile has read the copy of S too
+          if (!(ok = join(c, ds_full, c & 1, ds_addr))) break;
+          if (c + 1 < nt) publish();
+        }
+        bad = bad_next;
       } else {
+        const float f = r < Lt ? pwv[Lt - 1 - r] : 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint4 x = lds16(chunk(c, L::kV, i));
+          uint4 hi, lo;
+          split_pair(x.x, f, &hi.x, &lo.x);
+          split_pair(x.y, f, &hi.y, &lo.y);
+          split_pair(x.z, f, &hi.z, &lo.z);
+          split_pair(x.w, f, &hi.w, &lo.w);
+          sts16(chunk(c, L::kV, i), hi);
+          sts16(chunk(c, L::kQ, i), lo);
+        }
+        tc::fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(c & 1 ? s_full : o_empty);
+        if (lane == 0) tc::mbar_arrive(c & 1 ? v_hi : kv_ok);
+        // the next tile's parts are written while this one is multiplied
+        if (c > 0 && !(ok = join(c - 1, ds_full + ((c - 1) & 1), ((c - 1) >> 1) & 1, ds_addr - 128 * ((c - 1) & 1)))) break;
+        if (c + 1 < nt) ok = enter(c + 1, &bad_next);
       }
     }
-    if (ok && s_dst) {
+    if (!kOut && ok)
+      ok = join(nt - 1, ds_full + ((nt - 1) & 1), ((nt - 1) >> 1) & 1, ds_addr - 128 * ((nt - 1) & 1));
+    if (ok && mine && s_dst) {
 #pragma unroll
-      for (int e = 0; e < D; e += 4)
-        *reinterpret_cast<float4*>(s_dst + e) = make_float4(S[e], S[e + 1], S[e + 2], S[e + 3]);
+      for (int e = 0; e < 64; e += 4)
+        *reinterpret_cast<float4*>(s_dst + sc + e) = make_float4(S[e], S[e + 1], S[e + 2], S[e + 3]);
     }
   }
 
@@ -687,7 +778,7 @@ linear_packed_scan_kernel(const float* __restrict__ lambda, const int32_t* __res
   const long long e = 4 * ((long long)blockIdx.x * kPlScanThreads + threadIdx.x);
   const long long per = (long long)H * D * D;
   if (e >= per) return;
-  const float f = (float)pow((double)lambda[e / (D * D)], (double)seg_tokens);
+  const float f = decay_pow(lambda[e / (D * D)], seg_tokens);
   float4 S = make_float4(0.f, 0.f, 0.f, 0.f);
   if (state_in && slot >= 0) S = *reinterpret_cast<const float4*>(state_in + slot * per + e);
   float* p = ws + u.ws * per + e;

@@ -378,9 +378,9 @@ def sparse_prefill(q_norm, k_norm, v, gate, idx, *, block=64, topk=16, n_init=1,
 
 def _expect(name: str, t: torch.Tensor, shape, dtype, device):
     """The helpers below check what the C entry points cannot see: a tensor's shape, type and device."""
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise ValueError(f"{name}: {t.dtype}, expected {dtype}")
     if t.device != device:
         raise ValueError(f"{name}: on {t.device}, expected {device}")
@@ -388,32 +388,47 @@ def _expect(name: str, t: torch.Tensor, shape, dtype, device):
         raise ValueError(f"{name}: must be contiguous")
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _packed_call(what: str, device, fn, desc, tensors, ws, stream):
     """Launch on the tensors' own device, on its current stream unless one is given.  ``ws``: None for
     a call that takes no workspace, else (tensor or None, bytes needed)."""
     if device.type != "cuda":
         raise ValueError(f"{what}: tensors must be on a CUDA device")
-    with torch.cuda.device(device):
-        if stream is None:
-            stream = torch.cuda.current_stream(device)
-        args = [ctypes.byref(desc)] + [None if t is None else t.data_ptr() for t in tensors]
-        if ws is not None:
-            t, need = ws
-            if t is None and need > 0:
-                with torch.cuda.stream(stream):   # freed memory is reused in this stream's order
-                    t = workspace(need, device)
-            elif t is not None and (t.device != device or not t.is_contiguous()):
-                raise ValueError("ws: a contiguous tensor on the call's device")
-            args += [None if t is None else t.data_ptr(), 0 if t is None else t.numel() * t.element_size()]
-        _check(fn(*args, stream.cuda_stream), what)
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return _packed_call(what, device, fn, desc, tensors, ws, stream)
+    args = [None if t is None else t.data_ptr() for t in tensors]
+    if ws is not None:
+        t, need = ws
+        if t is None and need > 0:
+            t = _empty(need, torch.uint8, device, stream)
+        elif t is not None and (t.device != device or not t.is_contiguous()):
+            raise ValueError("ws: a contiguous tensor on the call's device")
+        args += [None, 0] if t is None else [t.data_ptr(), t.numel() * t.element_size()]
+    if stream is not None:
+        raw = stream.cuda_stream
+    elif _raw_stream is not None:
+        raw = _raw_stream(device.index)
+    else:
+        raw = torch.cuda.current_stream(device).cuda_stream
+    status = fn(ctypes.byref(desc), *args, raw)
+    if status != SALA_OK:
+        raise SalaError(status, what)
+
+
+def _empty(shape, dtype, device, stream):
+    """Memory that is reused in the order of the stream it was used on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def _out(out, shape, dtype, device, stream):
     if out is None:
-        if stream is None:
-            return torch.empty(shape, dtype=dtype, device=device)
-        with torch.cuda.stream(stream):
-            return torch.empty(shape, dtype=dtype, device=device)
+        return _empty(shape, dtype, device, stream)
     _expect("out", out, shape, dtype, device)
     return out
 
