@@ -100,6 +100,21 @@ inline bool make_tmap_bf16(CUtensorMap* map, const void* base, uint64_t cols, ui
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// 2D fp32 view [rows, cols] in boxes of box_cols (32: 128 bytes) x box_rows,
+// 128-byte swizzle.
+inline bool make_tmap_f32(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows, uint32_t box_cols,
+                          uint32_t box_rows) {
+  auto fn = get_encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {cols, rows};
+  cuuint64_t strides[1] = {cols * 4};
+  cuuint32_t box[2] = {box_cols, box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // 3D bf16 view [tokens, heads, D]: boxes of 64 columns x box_heads x
 // box_tokens, rows of 128 bytes ordered by token, then head (128-byte swizzle).
 inline bool make_tmap_rows(CUtensorMap* map, const void* base, uint64_t D, uint64_t heads, uint64_t tokens,

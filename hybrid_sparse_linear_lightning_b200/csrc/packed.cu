@@ -139,7 +139,8 @@ sala_status run_dense(const sala_dense_desc* d, const void* q, const void* k, co
 struct LinearPlan {
   int seg_tokens;
   int64_t extra;        // most segments behind a sequence's first
-  size_t total;         // workspace: states that enter them
+  int64_t entries;      // and with the first ones of these sequences
+  size_t total;         // workspace: the states that enter them
 };
 
 LinearPlan linear_plan(const sala_packed_linear_desc* d) {
@@ -154,7 +155,8 @@ LinearPlan linear_plan(const sala_packed_linear_desc* d) {
   seg = std::min<int64_t>(std::max<int64_t>(seg, 4), 1 << 20);
   p.seg_tokens = (int)(seg * kPlTile);
   p.extra = d->tokens / p.seg_tokens;
-  p.total = align_up((size_t)p.extra * d->heads * d->head_dim * d->head_dim * sizeof(float));
+  p.entries = p.extra + std::min<int64_t>(p.extra, d->n_seqs);
+  p.total = align_up((size_t)p.entries * d->heads * d->head_dim * d->head_dim * sizeof(float));
   return p;
 }
 
@@ -164,11 +166,20 @@ sala_status run_linear(const sala_packed_linear_desc* d, const void* q, const vo
                        const float* state_in, float* state_out, void* out, float* ws, cudaStream_t st) {
   const LinearPlan p = linear_plan(d);
   const int64_t groups = (d->heads + 128 / D - 1) / (128 / D);
-  CUtensorMap qm, km, vm;
+  CUtensorMap qm, km, vm, gm;
   const uint64_t cols = (uint64_t)d->heads * D;
   if (!make_tmap_bf16(&qm, q, cols, d->tokens, 64, kPlTile) ||
       !make_tmap_bf16(&km, k, cols, d->tokens, 64, kPlTile) ||
-      !make_tmap_bf16(&vm, v, cols, d->tokens, 64, kPlTile))
+      !make_tmap_bf16(&vm, v, cols, d->tokens, 64, kPlTile) ||
+      !make_tmap_bf16(&gm, gate, cols, d->tokens, 64, kPlTile))
+    return SALA_ERR_CUDA;
+  // states as rows of D fp32, read and written in boxes of 32 columns x one head
+  CUtensorMap sim = {}, som = {}, wsm = {};
+  const uint64_t rows = (uint64_t)d->n_slots * d->heads * D, ws_rows = (uint64_t)p.entries * d->heads * D;
+  if (rows > 0x7fffffffull || ws_rows > 0x7fffffffull) return SALA_ERR_UNSUPPORTED;
+  if ((state_in && !make_tmap_f32(&sim, state_in, D, rows, 32, D)) ||
+      (state_out && !make_tmap_f32(&som, state_out, D, rows, 32, D)) ||
+      (p.extra > 0 && !make_tmap_f32(&wsm, ws, D, ws_rows, 32, D)))
     return SALA_ERR_CUDA;
   const size_t smem = PlLayout::kBytes + 1024;
   const int64_t units = (p.extra + d->n_seqs) * groups;
@@ -177,8 +188,8 @@ sala_status run_linear(const sala_packed_linear_desc* d, const void* q, const vo
   auto launch = [&](auto kern, int64_t grid, std::atomic<uint64_t>* done) {
     if (allow_smem_once(kern, smem, done) != cudaSuccess) return SALA_ERR_CUDA;
     kern<<<(unsigned)grid, kPlThreads, smem, st>>>(
-        qm, km, vm, static_cast<const bf16*>(v), static_cast<const bf16*>(gate), lambda, cu, slots, state_in,
-        state_out, ws, static_cast<bf16*>(out), d->tokens, d->n_seqs, d->n_slots, d->heads, p.seg_tokens,
+        qm, km, vm, gm, sim, som, wsm, static_cast<const bf16*>(v), static_cast<const bf16*>(gate), lambda, cu,
+        slots, state_in, state_out, static_cast<bf16*>(out), d->tokens, d->n_seqs, d->n_slots, d->heads, p.seg_tokens,
         d->scale);
     return launch_status();
   };

@@ -174,7 +174,8 @@ __device__ __forceinline__ void pa_run(const CUtensorMap& qmap, const CUtensorMa
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMisc);
   volatile int* found = reinterpret_cast<volatile int*>(smem + L::kMisc + 4);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // the same in all lanes, and known to be: branches on it are uniform
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int G = Hq / Hkv;
   const int nb = max(job.nb[0], job.nb[1]);
 

@@ -41,10 +41,10 @@ namespace sala {
 
 constexpr int kPlThreads = 512;
 constexpr int kPlTile = 128;
-// warpgroup 0: TMA, MMA, TMEM; 1 and 3: V and the state, half the columns each;
-// 2: P and outputs.  The shares sum to the 4 x 128 registers that the block is
+// warpgroup 0: TMA, MMA, TMEM; 1 and 3: P, V and the state, half the columns
+// each; 2: outputs.  The shares sum to the 4 x 128 registers that the block is
 // launched with.
-constexpr int kPlRegs0 = 56, kPlRegsV = 152, kPlRegs2 = 152;
+constexpr int kPlRegs0 = 56, kPlRegsV = 176, kPlRegs2 = 104;
 static_assert(kPlRegs0 + 2 * kPlRegsV + kPlRegs2 <= 4 * 128, "register split exceeds the launch");
 
 struct PlLayout {
@@ -54,10 +54,33 @@ struct PlLayout {
   static constexpr int kPw = kS + 32768;                   // lam^m, m = 0..128, per head: [2][132]
   static constexpr int kBar = kPw + 2 * 132 * 4;
   // ld_full[2], ld_empty[2], kv_ok, qk_full, p_full, pv_done, o_full, o_empty, s_full, v_hi, v_lo,
-  // hi_done, ds_full[2], fin
-  static constexpr int kNumBars = 17;
+  // hi_done, ds_full[2], fin, s_ld, e_sync, v_sync
+  static constexpr int kNumBars = 20;
+  // Barriers by their byte offset.  Every barrier's phase is waited for by all who
+  // wait on it before the next one can complete.  Where kOut is false, tiles of
+  // even and odd number use kv_ok and v_hi (V' written) in turn for that.
+  enum : uint32_t {
+    ld_full = 0,         // [2] Q, K, V of a tile have landed
+    ld_empty = 16,       // [2] products done, and outputs written
+    kv_ok = 32,          // rows past the end and non-finite values are 0
+    qk_full = 40,
+    p_full = 48,
+    pv_done = 56,        // V may be overwritten by V'
+    o_full = 64,
+    o_empty = 72,
+    s_full = 80,         // the bf16 copy of S
+    v_hi = 88,
+    v_lo = 96,
+    hi_done = 104,
+    ds_full = 112,       // [2]
+    fin = 128,
+    s_ld = 136,          // the entering state has landed
+    e_sync = 144,        // among the warps that write outputs
+    v_sync = 152,        // the leaving state lies in shared memory
+  };
   static constexpr int kMisc = kBar + 8 * kNumBars;        // TMEM address, unit, found[2][8]
-  static constexpr int kBytes = kMisc + 128;
+  static constexpr int kShared = kMisc + 96;               // PlShared
+  static constexpr int kBytes = kShared + 64;
   static constexpr int kColQK = 0, kColO1 = 128, kColO2 = 256, kColDs = 384;
   static_assert(kBar % 8 == 0 && kMisc % 8 == 0, "alignment");
 };
@@ -73,13 +96,24 @@ __device__ __forceinline__ float decay_pow(float lam, int n) {
   return (float)p;
 }
 
+// Read by the roles where they need it.
+struct PlShared {
+  const __nv_bfloat16 *v, *gate;
+  __nv_bfloat16* out;
+  const CUtensorMap* dst_map;      // of the leaving state
+  int dst_row;                     // its first row, -1 for nowhere
+  int s0, H, hg;
+  float scale;
+};
+static_assert(sizeof(PlShared) <= 64, "its place in shared memory");
+
 // How a call's sequences are cut: segments of seg_tokens.  What a CTA finds
 // for its index p among the sequences' segments (all of them, or all but each
 // sequence's last).
 struct PlUnit {
   int seq, seg;      // sequence, segment in it; seq < 0: none
   int n_seg;         // segments of the sequence
-  int ws;            // where the sequence's segment states begin
+  int ws;            // where the sequence's segment states begin (none where it has one segment)
 };
 
 // Called by one warp.
@@ -91,7 +125,7 @@ __device__ __forceinline__ PlUnit find_segment(const int32_t* cu, int n_seqs, in
     const int i = i0 + lane;
     int n = 0;
     if (i < n_seqs && seq_ok(cu, i, tokens)) n = max(1, (cu[i + 1] - cu[i] + seg_tokens - 1) / seg_tokens);
-    const int e = max(n - 1, 0), own = all ? n : e;
+    const int e = n > 1 ? n : 0, own = all ? n : max(n - 1, 0);
     int inc = own, ince = e;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -118,11 +152,17 @@ __device__ __forceinline__ PlUnit find_segment(const int32_t* cu, int n_seqs, in
 }
 
 // A load that stays where it is written: the compiler would else move it to
-// its first use, behind the wait that is to cover its latency.
+// its first use, behind the wait that is to cover its latency.  Gates and outputs
+// pass the L1 cache by: what shared memory leaves of it keeps spilled registers.
 __device__ __forceinline__ uint4 ld_now(const __nv_bfloat16* p) {
   uint4 u;
-  asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "l"(p));
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "l"(p));
   return u;
+}
+
+__device__ __forceinline__ void st_out(__nv_bfloat16* p, const uint4& u) {
+  asm volatile("st.global.L1::no_allocate.v4.u32 [%0], {%1,%2,%3,%4};" ::"l"(p), "r"(u.x), "r"(u.y), "r"(u.z), "r"(u.w)
+               : "memory");
 }
 
 // 16 bytes of shared memory by its 32-bit address.
@@ -154,6 +194,14 @@ __device__ __forceinline__ uint4 gate_pack(const uint4& g, const uint4& a, const
   return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
+// 2D tiled store of one box.
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t src, int x, int y) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(src), "r"(x), "r"(y)
+               : "memory");
+}
+
 // bf16 pair (w) times (f, f): high and low bf16 parts.
 __device__ __forceinline__ void split_pair(uint32_t w, float f, uint32_t* hi, uint32_t* lo) {
   const float2 x = __fmul2_rn(__bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w)), make_float2(f, f));
@@ -164,43 +212,448 @@ __device__ __forceinline__ void split_pair(uint32_t w, float f, uint32_t* hi, ui
   *lo = *reinterpret_cast<const uint32_t*>(&l);
 }
 
+// The warps that build P, split V and carry the state.  A function of its own,
+// not inlined: its registers are then allocated apart from the other roles'
+// (inlined, the compiler keeps 30 of them in memory inside the loop over tiles).
+// What it needs rarely is in shared memory (PlShared), not among its arguments,
+// which the compiler would keep in memory too.
+template <int D, bool kOut>
+__device__ __noinline__ void linear_state_role(uint32_t o_smem, uint32_t tmem, int n_tok, int nds, int flags) {
+  using L = PlLayout;
+  constexpr int NH = 128 / D;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const bool has_src = flags & 1;
+  const int nt = (n_tok + kPlTile - 1) / kPlTile, heads = flags >> 1;
+  // --------------------------------------------- V and the state (half the columns each)
+  tc::setmaxnreg_inc<kPlRegsV>();
+  auto o_len = [&](int c) { return min(kPlTile, n_tok - c * kPlTile); };
+  const uint32_t bar = o_smem + L::kBar;
+  const float* pw = reinterpret_cast<const float*>(__cvta_shared_to_generic(o_smem + L::kPw));
+  volatile int* found = reinterpret_cast<volatile int*>(__cvta_shared_to_generic(o_smem + L::kMisc + 32));
+  const volatile PlShared* sh = reinterpret_cast<const volatile PlShared*>(__cvta_shared_to_generic(o_smem + L::kShared));
+  const int r_own = threadIdx.x & 127, hsub = r_own / D;
+  const int quad = warp & 3, half = warp >= 12;
+  const int r = r_own;                      // token row of V, key row of S (of head hsub)
+  // 16-byte chunk i (of 8) of this half row of the tile at offset `part` of stage c & 1
+  const uint32_t row_a = o_smem + half * 16384 + r * 128 + ((r & 7) << 4);
+  auto chunk = [&](int c, int part, int i) { return (row_a + (c & 1) * L::kStage + part) ^ (i << 4); };
+  // makes the tile safe to multiply; says whether this part of V held values
+  // that are not finite (they are 0 now).  False where a wait ran out.
+  auto enter = [&](int c, bool* bad) {
+    if (!__all_sync(0xffffffffu, tc::mbar_wait(bar + L::ld_full + 8 * (c & 1), (c >> 1) & 1))) return false;
+    *bad = false;
+    if (r >= o_len(c)) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        sts16(chunk(c, L::kV, i), make_uint4(0, 0, 0, 0));
+        sts16(chunk(c, L::kK, i), make_uint4(0, 0, 0, 0));
+      }
+    } else if (kOut) {
+      uint32_t acc = 0;
+#pragma unroll 1
+      for (int i0 = 0; i0 < 8; i0 += 4) {
+        uint4 x[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = lds16(chunk(c, L::kV, i0 + i));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {      // an exponent of ones carries into bit 15 of its half
+        acc |= ((x[i].x & 0x7f807f80u) + 0x00800080u) | ((x[i].y & 0x7f807f80u) + 0x00800080u);
+        acc |= ((x[i].z & 0x7f807f80u) + 0x00800080u) | ((x[i].w & 0x7f807f80u) + 0x00800080u);
+      }
+      }
+      *bad = (acc & 0x80008000u) != 0;
+      if (*bad) {
+#pragma unroll 1
+        for (int i = 0; i < 8; ++i) {
+          const uint4 x = lds16(chunk(c, L::kV, i));
+          const unsigned m = nonfinite8(x);
+          uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if (m >> (2 * e) & 1) w[e] &= 0xffff0000u;
+            if (m >> (2 * e + 1) & 1) w[e] &= 0xffffu;
+          }
+          sts16(chunk(c, L::kV, i), make_uint4(w[0], w[1], w[2], w[3]));
+        }
+      }
+    }
+    if (kOut) {
+      const bool any = __any_sync(0xffffffffu, *bad);
+      if (lane == 0) found[(c & 1) * 8 + half * 4 + quad] = any;
+      tc::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(bar + L::kv_ok);
+    }
+    return true;
+  };
+  const float* pwv = pw + (NH == 1 ? 0 : half) * 132;     // decays of the half's head
+  // the state: columns [64 half, 64 half + 64) of row r; where two heads lie
+  // side by side only the half of the row's own head
+  const bool mine = NH == 1 || half == hsub;
+  const uint32_t ds_addr = tmem + ((uint32_t)(quad * 32) << 16) + L::kColDs + 64 * half;
+  // where the row's 64 columns lie while the state is loaded or stored: boxes of
+  // 32 columns, swizzled like the tiles
+  const uint32_t box_a = o_smem + L::kK + (hsub * (D / 32) + (NH == 1 ? 2 * half : 0)) * (D * 128) + (r % D) * 128 +
+                         ((r & 7) << 4);
+  float S[64];
+#pragma unroll
+  for (int e = 0; e < 64; ++e) S[e] = 0.f;
+  bool ok = true;
+  if (has_src) {
+    ok = __all_sync(0xffffffffu, tc::mbar_wait(bar + L::s_ld, 0));
+    if (ok && mine && hsub < heads) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const uint4 x = lds16((box_a + L::kStage + (i >> 3) * (D * 128)) ^ ((i & 7) << 4));
+        S[4 * i] = __uint_as_float(x.x);
+        S[4 * i + 1] = __uint_as_float(x.y);
+        S[4 * i + 2] = __uint_as_float(x.z);
+        S[4 * i + 3] = __uint_as_float(x.w);
+      }
+    }
+  }
+  auto publish = [&]() {
+    if (mine) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const __nv_bfloat162 h2 = __floats2bfloat162_rn(S[8 * i + 2 * e], S[8 * i + 2 * e + 1]);
+          w[e] = *reinterpret_cast<const uint32_t*>(&h2);
+        }
+        sts16(chunk(0, L::kS, i), make_uint4(w[0], w[1], w[2], w[3]));
+      }
+    }
+    tc::fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(bar + L::s_full);
+  };
+  // S <- lam^L S + K^T V' of tile c
+  auto join = [&](int c, uint32_t full, int parity, uint32_t src) {
+    if (!__all_sync(0xffffffffu, tc::mbar_wait(full, parity))) return false;
+    tc::tc_fence_after();
+    const float f = pw[hsub * 132 + o_len(c)];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float x[16];
+      tc::tmem_ld16(src + 16 * j, x);
+      tc::tmem_wait_ld();
+#pragma unroll
+      for (int e = 0; e < 16; ++e) S[16 * j + e] = fmaf(f, S[16 * j + e], x[e]);
+    }
+    tc::tc_fence_before();
+    return true;
+  };
+  // P of one head: (Q K^T)_rj lam^(r-j) for j <= r, this half's 64 columns.
+  // Its bf16 pairs take the first 32 of the columns that it read.
+  auto make_p = [&](int c, int hs) {
+    if (!__all_sync(0xffffffffu, tc::mbar_wait(bar + L::qk_full, (c * NH + hs) & 1))) return false;
+    tc::tc_fence_after();
+    const float* pwh = pw + hs * 132;
+    const uint32_t qk = tmem + ((uint32_t)(quad * 32) << 16) + L::kColQK + 64 * half;
+#pragma unroll 1
+    for (int x0 = 0; x0 < 2; ++x0) {
+      const int q0 = 2 * half + x0;         // 32-column chunk
+      uint32_t pk[16];
+      if (q0 <= quad) {
+        float xv[32];
+        tc::tmem_ld32(qk + 32 * x0, xv);
+        tc::tmem_wait_ld();
+        if (q0 == quad) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const float d = pwh[max(lane - e, 0)];
+            xv[e] = e <= lane ? xv[e] * d : 0.f;
+          }
+        } else {
+          // element e decays by lam^(a - e): four pairs with powers of their own,
+          // lam^8 from one to the next, from the largest power down
+          const int a = r - 32 * q0;
+          float2 dcy[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) dcy[x] = make_float2(pwh[a - 24 - 2 * x], pwh[a - 25 - 2 * x]);
+          const float2 l8 = make_float2(pwh[8], pwh[8]);
+#pragma unroll
+          for (int e0 = 24; e0 >= 0; e0 -= 8)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const int e = e0 + 2 * x;
+              const float2 y = __fmul2_rn(make_float2(xv[e], xv[e + 1]), dcy[x]);
+              xv[e] = y.x;
+              xv[e + 1] = y.y;
+              dcy[x] = __fmul2_rn(dcy[x], l8);
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const __nv_bfloat162 h2 = __floats2bfloat162_rn(xv[2 * e], xv[2 * e + 1]);
+          pk[e] = *reinterpret_cast<const uint32_t*>(&h2);
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) pk[e] = 0u;
+      }
+      tc::tmem_st16_u(qk + 16 * x0, pk);
+    }
+    tc::tmem_wait_st();
+    tc::tc_fence_before();
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(bar + L::p_full);
+    return true;
+  };
+  bool bad = false, bad_next = false;
+  if (kOut && ok) publish();
+  // kOut: round c finishes tile c and begins tile c + 1
+  if (!kOut) ok = ok && enter(0, &bad);
+#pragma unroll 1
+  for (int c = kOut ? -1 : 0; ok && c < nt; ++c) {
+    const int Lt = o_len(c);
+    if constexpr (kOut) {
+      const bool want = c >= 0 && c < nds;
+      if (c >= 0 && !(ok = __all_sync(0xffffffffu, tc::mbar_wait(bar + L::pv_done, c & 1)))) break;
+      uint4 lo[8] = {};
+      if (want) {
+        const float f = r < Lt ? pwv[Lt - 1 - r] : 0.f;
+        if (bad) {         // the state takes the row as it came
+          const __nv_bfloat16* vr = sh->v + (long long)(sh->s0 + c * kPlTile + r) * sh->H * D + sh->hg * 128 + 64 * half;
+#pragma unroll 1
+          for (int i = 0; i < 8; ++i) sts16(chunk(c, L::kV, i), *reinterpret_cast<const uint4*>(vr + 8 * i));
+        }
+#pragma unroll
+        for (int i0 = 0; i0 < 8; i0 += 4) {
+          uint4 x[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[i] = lds16(chunk(c, L::kV, i0 + i));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint4 hi;
+            split_pair(x[i].x, f, &hi.x, &lo[i0 + i].x);
+            split_pair(x[i].y, f, &hi.y, &lo[i0 + i].y);
+            split_pair(x[i].z, f, &hi.z, &lo[i0 + i].z);
+            split_pair(x[i].w, f, &hi.w, &lo[i0 + i].w);
+            sts16(chunk(c, L::kV, i0 + i), hi);
+          }
+        }
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(bar + L::v_hi);
+      }
+      if (c + 1 < nt && !(ok = enter(c + 1, &bad_next))) break;
+      if (want) {
+        if (!(ok = __all_sync(0xffffffffu, tc::mbar_wait(bar + L::hi_done, c & 1)))) break;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sts16(chunk(c, L::kV, i), lo[i]);
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(bar + L::v_lo);
+      }
+      if (c + 1 < nt) {
+#pragma unroll 1
+        for (int hs = 0; ok && hs < NH; ++hs) ok = make_p(c + 1, hs);
+        if (!ok) break;
+      }
+      if (want) {
+        // the products being done says that Q S of this tile has read the copy of S too
+        if (!(ok = join(c, bar + L::ds_full, c & 1, ds_addr))) break;
+        if (c + 1 < nt) publish();
+      }
+      bad = bad_next;
+    } else {
+      const float f = r < Lt ? pwv[Lt - 1 - r] : 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint4 x = lds16(chunk(c, L::kV, i));
+        uint4 hi, lo;
+        split_pair(x.x, f, &hi.x, &lo.x);
+        split_pair(x.y, f, &hi.y, &lo.y);
+        split_pair(x.z, f, &hi.z, &lo.z);
+        split_pair(x.w, f, &hi.w, &lo.w);
+        sts16(chunk(c, L::kV, i), hi);
+        sts16(chunk(c, L::kQ, i), lo);
+      }
+      tc::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(bar + (c & 1 ? L::v_hi : L::kv_ok));
+      // the next tile's parts are written while this one is multiplied
+      if (c > 0 && !(ok = join(c - 1, bar + L::ds_full + 8 * ((c - 1) & 1), ((c - 1) >> 1) & 1, ds_addr - 128 * ((c - 1) & 1)))) break;
+      if (c + 1 < nt) ok = enter(c + 1, &bad_next);
+    }
+  }
+  if (!kOut && ok)
+    ok = join(nt - 1, bar + L::ds_full + 8 * ((nt - 1) & 1), ((nt - 1) >> 1) & 1, ds_addr - 128 * ((nt - 1) & 1));
+  // every product and every load is done: the state leaves through stage 0
+  const int dst_row = sh->dst_row;
+  if (dst_row >= 0) {
+    if (ok) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (mine)
+          sts16((box_a + (i >> 3) * (D * 128)) ^ ((i & 7) << 4),
+                make_uint4(__float_as_uint(S[4 * i]), __float_as_uint(S[4 * i + 1]), __float_as_uint(S[4 * i + 2]),
+                           __float_as_uint(S[4 * i + 3])));
+    }
+    tc::fence_proxy_async_smem();
+    __syncwarp();
+    if (ok && lane == 0) tc::mbar_arrive(bar + L::v_sync);
+    if (warp == 4 && lane == 0 && ok && tc::mbar_wait(bar + L::v_sync, 0)) {
+      for (int i = 0; i < heads * (D / 32); ++i)
+        tma_store_2d(sh->dst_map, o_smem + L::kK + i * (D * 128), 32 * (i % (D / 32)),
+                     dst_row + i / (D / 32) * D);
+      asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group 0;" ::: "memory");
+    }
+    __syncwarp();
+  }
+}
+
+// The warps that write the outputs, a function of its own like the last.
+//
+// out = sigmoid(gate) scale (lam^(r+1) O1 + O2).  A thread holds a token's row,
+// whose neighbours lie H d values apart: 64 columns at a time go through the
+// tile's Q, which no product needs any more, so that gate and out are read and
+// written 128 bytes a row.
+template <int D>
+__device__ __noinline__ void linear_output_role(uint32_t o_smem, uint32_t tmem, int n_tok) {
+  using L = PlLayout;
+  tc::setmaxnreg_dec<kPlRegs2>();
+  const float* pw = reinterpret_cast<const float*>(__cvta_shared_to_generic(o_smem + L::kPw));
+  const volatile int* found =
+      reinterpret_cast<const volatile int*>(__cvta_shared_to_generic(o_smem + L::kMisc + 32));
+  const volatile PlShared* sh = reinterpret_cast<const volatile PlShared*>(__cvta_shared_to_generic(o_smem + L::kShared));
+  const int s0 = sh->s0, H = sh->H, hg = sh->hg;
+  const float scale = sh->scale;
+  const __nv_bfloat16* gate = sh->gate;
+  __nv_bfloat16* out = sh->out;
+  const uint32_t bar = o_smem + L::kBar;
+  const int quad = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31, r = threadIdx.x & 127;          // token row
+  const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
+  const int cols = min(128, H * D - hg * 128);           // columns of heads that exist
+  const int cr = quad * 4 + (lane >> 3), cq = lane & 7;      // row (+ 16 i) and 8-column chunk of a copy
+  const long long rs = (long long)H * D;                   // from token to token
+  uint32_t phase = 0;
+  auto sync = [&]() {              // the four warps, with a bound
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(bar + L::e_sync);
+    const bool ok = __all_sync(0xffffffffu, tc::mbar_wait(bar + L::e_sync, phase & 1));
+    ++phase;
+    return ok;
+  };
+#pragma unroll 1
+  for (int c = 0; kPlTile * c < n_tok; ++c) {
+    const int Lt = min(kPlTile, n_tok - c * kPlTile);
+    const long long t0 = s0 + c * kPlTile;
+    const long long at = (t0 + cr) * rs + hg * 128 + 8 * cq;
+    uint4 g[8];
+    auto load_gate = [&](int h) {
+      const __nv_bfloat16* p = gate + at + 64 * h;
+#pragma unroll
+      for (int i = 0; i < 8; ++i, p += 16 * rs)
+        if (cr + 16 * i < Lt && 64 * h < cols) g[i] = ld_now(p);
+    };
+    load_gate(0);
+    if (!__all_sync(0xffffffffu, tc::mbar_wait(bar + L::o_full, c & 1))) break;
+    tc::tc_fence_after();
+    const volatile int* fc = found + (c & 1) * 8;
+    const bool bad = fc[0] | fc[1] | fc[2] | fc[3] | fc[4] | fc[5] | fc[6] | fc[7];
+    // 16-byte chunk x of a row of 64 fp32 lies at place (x >> 1 | (x & 1) << 3) ^ (row & 7)
+    // of its 16: free of bank conflicts by rows and by pairs of chunks
+    const uint32_t stg = o_smem + (c & 1) * L::kStage + L::kQ;
+    const uint32_t put_a = stg + r * 256 + ((r & 7) << 4);
+    const uint32_t get_a = (stg + cr * 256 + ((cr & 7) << 4)) ^ (cq << 4);     // chunks 2 cq and 2 cq + 1
+    // 16 columns of the row into chunks x0 .. x0 + 3
+    auto combine = [&](int col, int x0, bool end) {
+      float o[16], o2[16];
+      tc::tmem_ld16(lane_base + L::kColO1 + col, o);
+      tc::tmem_ld16(lane_base + L::kColO2 + col, o2);
+      tc::tmem_wait_ld();
+      if (end) {
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(bar + L::o_empty);
+      }
+      const float f = scale * pw[(col / D) * 132 + r + 1];
+#pragma unroll
+      for (int e = 0; e < 16; e += 2) {
+        const float2 y = __ffma2_rn(make_float2(f, f), make_float2(o[e], o[e + 1]),
+                                    __fmul2_rn(make_float2(scale, scale), make_float2(o2[e], o2[e + 1])));
+        o[e] = y.x;
+        o[e + 1] = y.y;
+      }
+      if (bad && r < Lt && col < cols) {       // the values of V that P V left out
+        for (int t = 0; t <= r; ++t) {
+          const __nv_bfloat16* vr = sh->v + (t0 + t) * rs + hg * 128 + col;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float x = to_f32(vr[e]);
+            if (!isfinite(x)) o[e] += x;
+          }
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        sts16(put_a ^ (x0 << 3) ^ ((x >> 1 | (x & 1) << 3) << 4), make_uint4(__float_as_uint(o[4 * x]), __float_as_uint(o[4 * x + 1]),
+                                              __float_as_uint(o[4 * x + 2]), __float_as_uint(o[4 * x + 3])));
+    };
+    // the staged half: gated and written
+    auto store = [&](int h) {
+      constexpr int kB = 4;            // rows of a thread at a time
+      __nv_bfloat16* p = out + at + 64 * h;
+#pragma unroll
+      for (int i0 = 0; i0 < 8; i0 += kB) {
+        uint4 a[kB], b[kB];
+#pragma unroll
+        for (int i = 0; i < kB; ++i) {
+          a[i] = lds16(get_a + (i0 + i) * 4096);
+          b[i] = lds16((get_a ^ 128) + (i0 + i) * 4096);
+        }
+#pragma unroll
+        for (int i = 0; i < kB; ++i) a[i] = gate_pack(g[i0 + i], a[i], b[i]);
+#pragma unroll
+        for (int i = 0; i < kB; ++i, p += 16 * rs)
+          if (cr + 16 * (i0 + i) < Lt && 64 * h < cols) st_out(p, a[i]);
+      }
+    };
+    // rolled: every role's straight-line code together would not fit the
+    // instruction caches
+    bool ok = true;
+#pragma unroll 1
+    for (int h = 0; ok && h < 2; ++h) {
+#pragma unroll 1
+      for (int j = 0; j < 4; ++j) combine(64 * h + 16 * j, 4 * j, h == 1 && j == 3);
+      if (!(ok = sync())) break;
+      store(h);
+      if (h == 0) load_gate(1);
+      else tc::fence_proxy_async_smem();      // the next load writes there
+      ok = sync();
+    }
+    if (!ok) break;
+    if (threadIdx.x == 256) tc::mbar_arrive(bar + L::ld_empty + 8 * (c & 1));
+  }
+}
+
 template <int D, bool kOut>
 __global__ void __launch_bounds__(kPlThreads, 1)
 linear_packed_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
-                     const __grid_constant__ CUtensorMap vmap, const __nv_bfloat16* __restrict__ v,
-                     const __nv_bfloat16* __restrict__ gate, const float* __restrict__ lambda,
+                     const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap gmap,
+                     const __grid_constant__ CUtensorMap simap, const __grid_constant__ CUtensorMap somap,
+                     const __grid_constant__ CUtensorMap wsmap, const __nv_bfloat16* __restrict__ v,
+                     const __nv_bfloat16* __restrict__ gate,
+                     const float* __restrict__ lambda,
                      const int32_t* __restrict__ cu, const int32_t* __restrict__ slots,
-                     const float* state_in, float* state_out, float* __restrict__ ws,
-                     __nv_bfloat16* __restrict__ out, int tokens, int n_seqs, int n_slots, int H,
+                     const float* state_in, float* state_out, __nv_bfloat16* __restrict__ out, int tokens, int n_seqs, int n_slots, int H,
                      int seg_tokens, float scale) {
   using L = PlLayout;
   constexpr int NH = 128 / D;               // heads side by side
   extern __shared__ __align__(1024) uint8_t smem_pl[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_pl) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBar);
-  // Every barrier's phase is waited for by all who wait on it before the next
-  // one can complete.  Where kOut is false, tiles of even and odd number use
-  // kv_ok and v_hi (V' written) in turn for that.
-  uint64_t* ld_full = bars;            // [2] Q, K, V of a tile have landed
-  uint64_t* ld_empty = bars + 2;       // [2]
-  uint64_t* kv_ok = bars + 4;          // rows past the end and non-finite values are 0
-  uint64_t* qk_full = bars + 5;
-  uint64_t* p_full = bars + 6;
-  uint64_t* pv_done = bars + 7;        // V may be overwritten by V'
-  uint64_t* o_full = bars + 8;
-  uint64_t* o_empty = bars + 9;
-  uint64_t* s_full = bars + 10;        // the bf16 copy of S
-  uint64_t* v_hi = bars + 11;
-  uint64_t* v_lo = bars + 12;
-  uint64_t* hi_done = bars + 13;
-  uint64_t* ds_full = bars + 14;       // [2]
-  uint64_t* fin = bars + 16;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMisc);
   PlUnit* unit = reinterpret_cast<PlUnit*>(smem + L::kMisc + 8);
   volatile int* found = reinterpret_cast<volatile int*>(smem + L::kMisc + 32);   // [2][8]
   float* pw = reinterpret_cast<float*>(smem + L::kPw);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // the same in all lanes, and known to be: branches on it are uniform
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int n_hg = (H + NH - 1) / NH;
   const int hg = blockIdx.x % n_hg;
   if (kOut && blockIdx.x == 0)
@@ -218,49 +671,48 @@ linear_packed_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
   const int n_tok = min(cu[u.seq + 1] - s0, seg_tokens);
   const int nt = (n_tok + kPlTile - 1) / kPlTile;
   const bool last = u.seg + 1 == u.n_seg;
-  // where this thread's state row lives: row r of the 128 is key dim r % D of head r / D
-  const int r_own = threadIdx.x & 127;
-  const int hsub = r_own / D, h_own = hg * NH + hsub;
-  const long long srow = (((long long)slot * H + h_own) * D + r_own % D) * D;
-  const float* s_src = nullptr;
-  if (h_own < H && kOut) {
-    if (u.seg > 0) s_src = ws + (((long long)(u.ws + u.seg - 1) * H + h_own) * D + r_own % D) * D;
-    else if (state_in && slot >= 0) s_src = state_in + srow;
-  }
-  float* s_dst = nullptr;
-  if (h_own < H) {
-    if (!kOut) s_dst = ws + (((long long)(u.ws + u.seg) * H + h_own) * D + r_own % D) * D;
-    else if (last && state_out && slot >= 0) s_dst = state_out + srow;
-  }
+  // the entering and the leaving state: rows of D values from `row` on, key dims
+  // of the heads one after the other
+  const bool has_src = kOut && (u.n_seg > 1 || (state_in && slot >= 0));
+  const bool has_dst = !kOut || (last && state_out && slot >= 0);
+  const int heads = min(NH, H - hg * NH);              // heads that exist
+  const int own_row = (slot * H + hg * NH) * D;        // in the caller's pools
   if (nt == 0) {        // an empty sequence hands its state on
-    if (threadIdx.x < 128 && s_dst)
-      for (int c = 0; c < D; c += 4)
-        *reinterpret_cast<float4*>(s_dst + c) =
-            s_src ? *reinterpret_cast<const float4*>(s_src + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+    if (has_dst)
+      for (int e = threadIdx.x; e < heads * D * D / 4; e += kPlThreads) {
+        const long long at = (long long)own_row * D + 4 * e;
+        *reinterpret_cast<float4*>(state_out + at) =
+            has_src ? *reinterpret_cast<const float4*>(state_in + at) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
     return;
   }
   // tiles whose K^T V' is wanted
-  const bool keep = !kOut || (last && state_out && slot >= 0);
-  const int nds = keep ? nt : nt - 1;
+  const int nds = has_dst ? nt : nt - 1;
   auto tile_len = [&](int c) { return min(kPlTile, n_tok - c * kPlTile); };
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
-      tc::mbar_init(ld_full + i, 1);
-      tc::mbar_init(ld_empty + i, kOut ? 2 : 1);     // products done, and outputs written
-      tc::mbar_init(ds_full + i, 1);
+      tc::mbar_init(bars + L::ld_full / 8 + i, 1);
+      tc::mbar_init(bars + L::ld_empty / 8 + i, kOut ? 2 : 1);     // products done, and outputs written
+      tc::mbar_init(bars + L::ds_full / 8 + i, 1);
     }
-    tc::mbar_init(kv_ok, 8);
-    tc::mbar_init(qk_full, 1);
-    tc::mbar_init(p_full, 4);
-    tc::mbar_init(pv_done, 1);
-    tc::mbar_init(o_full, 1);
-    tc::mbar_init(o_empty, 4);
-    tc::mbar_init(s_full, 8);
-    tc::mbar_init(v_hi, 8);
-    tc::mbar_init(v_lo, 8);
-    tc::mbar_init(hi_done, 1);
-    tc::mbar_init(fin, 1);
+    PlShared* sh = reinterpret_cast<PlShared*>(smem + L::kShared);
+    *sh = PlShared{v, gate, out, kOut ? &somap : &wsmap,
+                   !has_dst ? -1 : kOut ? own_row : ((u.ws + u.seg + 1) * H + hg * NH) * D, s0, H, hg, scale};
+    tc::mbar_init(bars + L::kv_ok / 8, 8);
+    tc::mbar_init(bars + L::qk_full / 8, 1);
+    tc::mbar_init(bars + L::p_full / 8, 8);
+    tc::mbar_init(bars + L::pv_done / 8, 1);
+    tc::mbar_init(bars + L::o_full / 8, 1);
+    tc::mbar_init(bars + L::o_empty / 8, 4);
+    tc::mbar_init(bars + L::s_full / 8, 8);
+    tc::mbar_init(bars + L::v_hi / 8, 8);
+    tc::mbar_init(bars + L::v_lo / 8, 8);
+    tc::mbar_init(bars + L::hi_done / 8, 1);
+    tc::mbar_init(bars + L::fin / 8, 1);
+    tc::mbar_init(bars + L::s_ld / 8, 1);
+    tc::mbar_init(bars + L::e_sync / 8, 4);
+    tc::mbar_init(bars + L::v_sync / 8, 8);
     tc::fence_barrier_init();
   }
   for (int e = threadIdx.x; e < NH * 129; e += kPlThreads) {
@@ -278,24 +730,37 @@ linear_packed_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
 
   if (warp < 4) {
     tc::setmaxnreg_dec<kPlRegs0>();
+    const uint32_t o_smem = tc::smem_u32(smem), bar = o_smem + L::kBar;
     if (warp == 0) {
       // ------------------------------------------------------------ TMA producer
       if (tc::elect_one()) {
         int c = 0;
         for (; c < nt; ++c) {
           const int st = c & 1, use = c >> 1;
-          if (use > 0 && !tc::mbar_wait(ld_empty + st, (use - 1) & 1)) break;
-          uint8_t* stage = smem + st * L::kStage;
-          tc::mbar_expect_tx(ld_full + st, kOut ? 98304 : 65536);
+          if (use > 0 && !tc::mbar_wait(bar + L::ld_empty + 8 * st, (use - 1) & 1)) break;
+          // stage 1 holds the entering state until its copy has been published
+          // (the next one cannot be before tile 1 is here)
+          if (c == 1 && has_src && !tc::mbar_wait(bar + L::s_full, 0)) break;
+          const uint32_t stage = o_smem + st * L::kStage;
+          tc::mbar_expect_tx(bar + L::ld_full + 8 * st, kOut ? 98304 : 65536);
           for (int a = 0; a < 2; ++a) {
             const int x = hg * 128 + 64 * a, y = s0 + c * kPlTile;
-            tc::tma_load_2d(stage + L::kK + a * 16384, &kmap, ld_full + st, x, y);
-            if (kOut) tc::tma_load_2d(stage + L::kQ + a * 16384, &qmap, ld_full + st, x, y);
-            tc::tma_load_2d(stage + L::kV + a * 16384, &vmap, ld_full + st, x, y);
+            tc::tma_load_2d(stage + L::kK + a * 16384, &kmap, bar + L::ld_full + 8 * st, x, y);
+            if (kOut) tc::tma_load_2d(stage + L::kQ + a * 16384, &qmap, bar + L::ld_full + 8 * st, x, y);
+            tc::tma_load_2d(stage + L::kV + a * 16384, &vmap, bar + L::ld_full + 8 * st, x, y);
+            if (kOut) tc::tma_prefetch_l2_2d(&gmap, x, y);     // its loads come a tile later
+          }
+          if (c == 0 && has_src) {
+            const int row = u.n_seg > 1 ? ((u.ws + u.seg) * H + hg * NH) * D : own_row;
+            tc::mbar_expect_tx(bar + L::s_ld, heads * D * D * 4);
+            for (int i = 0; i < heads * (D / 32); ++i)
+              tc::tma_load_2d(o_smem + L::kStage + L::kK + i * (D * 128), u.n_seg > 1 ? &wsmap : &simap, bar + L::s_ld,
+                              32 * (i % (D / 32)), row + i / (D / 32) * D);
           }
         }
+        if (has_src) tc::mbar_wait(bar + L::s_ld, 0);
         // no copy is in flight when this warp ends, whatever became of the others
-        for (int i = max(0, c - 2); i < c; ++i) tc::mbar_wait(ld_full + (i & 1), (i >> 1) & 1);
+        for (int i = max(0, c - 2); i < c; ++i) tc::mbar_wait(bar + L::ld_full + 8 * (i & 1), (i >> 1) & 1);
       }
     } else if (warp == 1) {
       // ------------------------------------------------------------ MMA issuer
@@ -303,7 +768,7 @@ linear_packed_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
         constexpr uint32_t id_kk = tc::idesc_bf16_f32(128, 128, false, false);   // A, B K-major
         constexpr uint32_t id_pv = tc::idesc_bf16_f32(128, D, false, true);      // B MN-major
         constexpr uint32_t id_nn = tc::idesc_bf16_f32(128, 128, true, true);     // A, B MN-major
-        const uint32_t base = tc::smem_u32(smem);
+        const uint32_t base = o_smem;
         const uint32_t sb = base + L::kS;
         auto part = [&](int c, int which) { return base + (c & 1) * L::kStage + which; };
         auto issue_qk = [&](int c, int hs) {
@@ -315,7 +780,7 @@ linear_packed_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
             tc::mma_bf16_ss(tmem + L::kColQK, tc::smem_desc_sw128(q + off, 16, 1024),
                             tc::smem_desc_sw128(k + off, 16, 1024), id_kk, x > 0);
           }
-          tc::mma_commit(qk_full);
+          tc::mma_commit(bar + L::qk_full);
         };
         auto issue_ds = [&](int c, int which, uint32_t col, bool acc) {
           const uint32_t k = part(c, L::kK), w = part(c, which);
@@ -325,7 +790,7 @@ linear_packed_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
                             tc::smem_desc_sw128(w + kk * 2048, 16384, 1024), id_nn, acc || kk > 0);
         };
         auto loaded = [&](int c) {
-          return tc::mbar_wait(ld_full + (c & 1), (c >> 1) & 1) && tc::mbar_wait(kv_ok, c & 1);
+          return tc::mbar_wait(bar + L::ld_full + 8 * (c & 1), (c >> 1) & 1) && tc::mbar_wait(bar + L::kv_ok, c & 1);
         };
         bool ok = true;
         if constexpr (kOut) {
@@ -336,22 +801,22 @@ linear_packed_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
           }
           for (int c = 0; ok && c < nt; ++c) {
             // O2 = P V, head by head
-            if (c > 0 && !(ok = tc::mbar_wait(o_empty, (c - 1) & 1))) break;
+            if (c > 0 && !(ok = tc::mbar_wait(bar + L::o_empty, (c - 1) & 1))) break;
 #pragma unroll
             for (int hs = 0; hs < NH; ++hs) {
-              if (!(ok = tc::mbar_wait(p_full, (c * NH + hs) & 1))) break;
+              if (!(ok = tc::mbar_wait(bar + L::p_full, (c * NH + hs) & 1))) break;
               tc::tc_fence_after();
               const uint32_t vv = part(c, L::kV) + hs * 16384;
 #pragma unroll
               for (int kk = 0; kk < 8; ++kk)
-                tc::mma_bf16_ts(tmem + L::kColO2 + hs * D, tmem + L::kColQK + kk * 8,
+                tc::mma_bf16_ts(tmem + L::kColO2 + hs * D, tmem + L::kColQK + (kk >> 2) * 64 + (kk & 3) * 8,
                                 tc::smem_desc_sw128(vv + kk * 2048, 16384, 1024), id_pv, kk > 0);
               if (hs + 1 < NH) issue_qk(c, hs + 1);
             }
             if (!ok) break;
-            tc::mma_commit(pv_done);
+            tc::mma_commit(bar + L::pv_done);
             // O1 = Q S
-            if (!(ok = tc::mbar_wait(s_full, c & 1))) break;
+            if (!(ok = tc::mbar_wait(bar + L::s_full, c & 1))) break;
             tc::tc_fence_after();
             const uint32_t q = part(c, L::kQ);
 #pragma unroll
@@ -362,14 +827,14 @@ linear_packed_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
                               tc::smem_desc_sw128(sb + hs * 16384 + kk * 2048, 16384, 1024), id_pv,
                               kk * 16 % D > 0);
             }
-            tc::mma_commit(o_full);
+            tc::mma_commit(bar + L::o_full);
             // K^T V', high parts, then (while the low parts are written) the next
             // tile's Q K^T, then the low parts
             if (c < nds) {
-              if (!(ok = tc::mbar_wait(v_hi, c & 1))) break;
+              if (!(ok = tc::mbar_wait(bar + L::v_hi, c & 1))) break;
               tc::tc_fence_after();
               issue_ds(c, L::kV, L::kColDs, false);
-              tc::mma_commit(hi_done);
+              tc::mma_commit(bar + L::hi_done);
             }
             if (c + 1 < nt) {
               if (!(ok = loaded(c + 1))) break;
@@ -377,352 +842,35 @@ linear_packed_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
               issue_qk(c + 1, 0);
             }
             if (c < nds) {
-              if (!(ok = tc::mbar_wait(v_lo, c & 1))) break;
+              if (!(ok = tc::mbar_wait(bar + L::v_lo, c & 1))) break;
               tc::tc_fence_after();
               issue_ds(c, L::kV, L::kColDs, true);
-              tc::mma_commit(ds_full);
-              tc::mma_commit(ld_empty + (c & 1));
+              tc::mma_commit(bar + L::ds_full);
+              tc::mma_commit(bar + L::ld_empty + 8 * (c & 1));
             }
           }
         } else {
           // high parts lie in V's place, low parts in Q's
           for (int c = 0; ok && c < nt; ++c) {
             const int x = c & 1, use = c >> 1;
-            if (!(ok = tc::mbar_wait(ld_full + x, use & 1) && tc::mbar_wait(x ? v_hi : kv_ok, use & 1))) break;
+            if (!(ok = tc::mbar_wait(bar + L::ld_full + 8 * x, use & 1) && tc::mbar_wait(bar + (x ? L::v_hi : L::kv_ok), use & 1))) break;
             // (who wrote V' of this tile has read the sum of tile c - 2 before)
             tc::tc_fence_after();
             issue_ds(c, L::kV, L::kColDs - 128 * (c & 1), false);
             issue_ds(c, L::kQ, L::kColDs - 128 * (c & 1), true);
-            tc::mma_commit(ds_full + (c & 1));
-            tc::mma_commit(ld_empty + (c & 1));
+            tc::mma_commit(bar + L::ds_full + 8 * (c & 1));
+            tc::mma_commit(bar + L::ld_empty + 8 * (c & 1));
           }
         }
-        tc::mma_commit(fin);
-        tc::mbar_wait(fin, 0);
+        tc::mma_commit(bar + L::fin);
+        tc::mbar_wait(bar + L::fin, 0);
       }
     }
   } else if (warp >= 8 && warp < 12) {
-    // ------------------------------------------------------- P and gated outputs
-    tc::setmaxnreg_inc<kPlRegs2>();
-    if constexpr (kOut) {
-      const int quad = warp & 3, r = r_own;      // token row
-      const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
-      const int cols = min(128, H * D - hg * 128);      // columns of heads that exist
-      for (int c = 0; c < nt; ++c) {
-        if (!__all_sync(0xffffffffu, tc::mbar_wait(kv_ok, c & 1))) break;
-        const volatile int* fc = found + (c & 1) * 8;
-        const bool bad = fc[0] | fc[1] | fc[2] | fc[3] | fc[4] | fc[5] | fc[6] | fc[7];
-        bool ok = true;
-#pragma unroll 1
-        for (int hs = 0; hs < NH; ++hs) {
-          if (!(ok = __all_sync(0xffffffffu, tc::mbar_wait(qk_full, (c * NH + hs) & 1)))) break;
-          tc::tc_fence_after();
-          const float* pwh = pw + hs * 132;
-          // 32-column chunk u of P (bf16 pairs) lands on columns [16 u, 16 u + 16),
-          // read with chunk u / 2 <= u: each is written back as it is built
-#pragma unroll
-          for (int q0 = 0; q0 < 4; ++q0) {
-            uint32_t pk[16];
-            if (q0 <= quad) {
-              float xv[32];
-              tc::tmem_ld32(lane_base + L::kColQK + 32 * q0, xv);
-              tc::tmem_wait_ld();
-              if (q0 == quad) {
-#pragma unroll
-                for (int e = 0; e < 32; ++e) xv[e] = e <= lane ? xv[e] * pwh[lane - e] : 0.f;
-              } else {
-                // element e decays by lam^(a - e): four pairs with powers of their own,
-                // lam^8 from one to the next, from the largest power down
-                const int a = r - 32 * q0;
-                float2 dcy[4];
-#pragma unroll
-                for (int x = 0; x < 4; ++x) dcy[x] = make_float2(pwh[a - 24 - 2 * x], pwh[a - 25 - 2 * x]);
-                const float2 l8 = make_float2(pwh[8], pwh[8]);
-#pragma unroll
-                for (int e0 = 24; e0 >= 0; e0 -= 8)
-#pragma unroll
-                  for (int x = 0; x < 4; ++x) {
-                    const int e = e0 + 2 * x;
-                    const float2 y = __fmul2_rn(make_float2(xv[e], xv[e + 1]), dcy[x]);
-                    xv[e] = y.x;
-                    xv[e + 1] = y.y;
-                    dcy[x] = __fmul2_rn(dcy[x], l8);
-                  }
-              }
-#pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                __nv_bfloat162 h2 = __floats2bfloat162_rn(xv[2 * e], xv[2 * e + 1]);
-                pk[e] = *reinterpret_cast<uint32_t*>(&h2);
-              }
-            } else {
-#pragma unroll
-              for (int e = 0; e < 16; ++e) pk[e] = 0u;
-            }
-            tc::tmem_st16_u(lane_base + L::kColQK + 16 * q0, pk);
-          }
-          tc::tmem_wait_st();
-          tc::tc_fence_before();
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive(p_full);
-        }
-        if (!ok) break;
-        // ---- out = sigmoid(gate) scale (lam^(r+1) O1 + O2)
-        // A thread holds a token's row, whose neighbours lie H d values apart:
-        // 64 columns at a time go through the tile's Q, which no product needs any
-        // more, so that gate and out are read and written 128 bytes a row.
-        const int Lt = tile_len(c);
-        const int cr = quad * 4 + (lane >> 3), cq = lane & 7;      // row (+ 16 i) and 8-column chunk
-        const long long at = (long long)(s0 + c * kPlTile + cr) * H * D + hg * 128 + 8 * cq;
-        uint4 g[8];
-        auto load_gate = [&](int h) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (cr + 16 * i < Lt && 64 * h < cols) g[i] = ld_now(gate + at + (long long)i * 16 * H * D + 64 * h);
-        };
-        load_gate(0);
-        if (!__all_sync(0xffffffffu, tc::mbar_wait(o_full, c & 1))) break;
-        tc::tc_fence_after();
-        // 16-byte chunk x of a row of 64 fp32: free of bank conflicts by rows and by columns
-        const uint32_t stg = tc::smem_u32(smem) + (c & 1) * L::kStage + L::kQ;
-        auto stage_at = [&](int row, int x) {
-          return (stg + row * 256 + ((row & 7) << 4)) ^ (((x >> 1) | ((x & 1) << 3)) << 4);
-        };
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float f = scale * pw[(64 * h / D) * 132 + r + 1];
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {                 // 32 columns at a time
-            float o1[32], o2[32];
-            tc::tmem_ld32(lane_base + L::kColO1 + 64 * h + 32 * j, o1);
-            tc::tmem_ld32(lane_base + L::kColO2 + 64 * h + 32 * j, o2);
-            tc::tmem_wait_ld();
-            if (h == 1 && j == 1) {
-              tc::tc_fence_before();
-              __syncwarp();
-              if (lane == 0) tc::mbar_arrive(o_empty);
-            }
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              const float2 y = __ffma2_rn(make_float2(f, f), make_float2(o1[e], o1[e + 1]),
-                                          __fmul2_rn(make_float2(scale, scale), make_float2(o2[e], o2[e + 1])));
-              o1[e] = y.x;
-              o1[e + 1] = y.y;
-            }
-            if (bad && r < Lt && 64 * h < cols) {
-              for (int t = 0; t <= r; ++t) {
-                const __nv_bfloat16* vr = v + (long long)(s0 + c * kPlTile + t) * H * D + hg * 128 + 64 * h + 32 * j;
-#pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                  const float x = to_f32(vr[e]);
-                  if (!isfinite(x)) o1[e] += x;
-                }
-              }
-            }
-#pragma unroll
-            for (int x = 0; x < 8; ++x)
-              sts16(stage_at(r, 8 * j + x),
-                    make_uint4(__float_as_uint(o1[4 * x]), __float_as_uint(o1[4 * x + 1]),
-                               __float_as_uint(o1[4 * x + 2]), __float_as_uint(o1[4 * x + 3])));
-          }
-          tc::named_sync(2, 128);
-          // all loads first: each thread's eight rows then overlap
-          uint4 a[8], b[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            a[i] = lds16(stage_at(cr + 16 * i, 2 * cq));
-            b[i] = lds16(stage_at(cr + 16 * i, 2 * cq + 1));
-          }
-#pragma unroll
-          for (int i = 0; i < 8; ++i) a[i] = gate_pack(g[i], a[i], b[i]);
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (cr + 16 * i < Lt && 64 * h < cols)
-              *reinterpret_cast<uint4*>(out + at + (long long)i * 16 * H * D + 64 * h) = a[i];
-          if (h == 0) load_gate(1);
-          if (h == 1) tc::fence_proxy_async_smem();      // the next load writes there
-          tc::named_sync(2, 128);
-        }
-        if (threadIdx.x == 256) tc::mbar_arrive(ld_empty + (c & 1));
-      }
-    }
+    if constexpr (kOut) linear_output_role<D>(tc::smem_u32(smem), tmem, n_tok);
+    else tc::setmaxnreg_dec<kPlRegs2>();
   } else {
-    // --------------------------------------------- V and the state (half the columns each)
-    tc::setmaxnreg_inc<kPlRegsV>();
-    const int quad = warp & 3, half = warp >= 12;
-    const int r = r_own;                      // token row of V, key row of S (of head hsub)
-    // 16-byte chunk i (of 8) of this half row of the tile at offset `part` of stage c & 1
-    const uint32_t row_a = tc::smem_u32(smem) + half * 16384 + r * 128 + ((r & 7) << 4);
-    auto chunk = [&](int c, int part, int i) { return (row_a + (c & 1) * L::kStage + part) ^ (i << 4); };
-    // makes the tile safe to multiply; says whether this part of V held values
-    // that are not finite (they are 0 now).  False where a wait ran out.
-    auto enter = [&](int c, bool* bad) {
-      if (!__all_sync(0xffffffffu, tc::mbar_wait(ld_full + (c & 1), (c >> 1) & 1))) return false;
-      *bad = false;
-      if (r >= tile_len(c)) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          sts16(chunk(c, L::kV, i), make_uint4(0, 0, 0, 0));
-          sts16(chunk(c, L::kK, i), make_uint4(0, 0, 0, 0));
-        }
-      } else if (kOut) {
-        uint32_t acc = 0;
-        uint4 x[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = lds16(chunk(c, L::kV, i));
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {      // an exponent of ones carries into bit 15 of its half
-          acc |= ((x[i].x & 0x7f807f80u) + 0x00800080u) | ((x[i].y & 0x7f807f80u) + 0x00800080u);
-          acc |= ((x[i].z & 0x7f807f80u) + 0x00800080u) | ((x[i].w & 0x7f807f80u) + 0x00800080u);
-        }
-        *bad = (acc & 0x80008000u) != 0;
-        if (*bad) {
-#pragma unroll 1
-          for (int i = 0; i < 8; ++i) {
-            const uint4 x = lds16(chunk(c, L::kV, i));
-            const unsigned m = nonfinite8(x);
-            uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              if (m >> (2 * e) & 1) w[e] &= 0xffff0000u;
-              if (m >> (2 * e + 1) & 1) w[e] &= 0xffffu;
-            }
-            sts16(chunk(c, L::kV, i), make_uint4(w[0], w[1], w[2], w[3]));
-          }
-        }
-      }
-      if (kOut) {
-        const bool any = __any_sync(0xffffffffu, *bad);
-        if (lane == 0) found[(c & 1) * 8 + half * 4 + quad] = any;
-        tc::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(kv_ok);
-      }
-      return true;
-    };
-    const float* pwv = pw + (NH == 1 ? 0 : half) * 132;     // decays of the half's head
-    // the state: columns [64 half, 64 half + 64) of row r; where two heads lie
-    // side by side only the half of the row's own head
-    const bool mine = NH == 1 || half == hsub;
-    const uint32_t ds_addr = tmem + ((uint32_t)(quad * 32) << 16) + L::kColDs + 64 * half;
-    const int sc = NH == 1 ? 64 * half : 0;                 // first column within the head
-    float S[64];
-#pragma unroll
-    for (int e = 0; e < 64; e += 4) {
-      const float4 x = mine && s_src ? __ldcg(reinterpret_cast<const float4*>(s_src + sc + e))
-                                     : make_float4(0.f, 0.f, 0.f, 0.f);
-      S[e] = x.x;
-      S[e + 1] = x.y;
-      S[e + 2] = x.z;
-      S[e + 3] = x.w;
-    }
-    auto publish = [&]() {
-      if (mine) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          uint32_t w[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const __nv_bfloat162 h2 = __floats2bfloat162_rn(S[8 * i + 2 * e], S[8 * i + 2 * e + 1]);
-            w[e] = *reinterpret_cast<const uint32_t*>(&h2);
-          }
-          sts16(chunk(0, L::kS, i), make_uint4(w[0], w[1], w[2], w[3]));
-        }
-      }
-      tc::fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(s_full);
-    };
-    // S <- lam^L S + K^T V' of tile c
-    auto join = [&](int c, uint64_t* full, int parity, uint32_t src) {
-      if (!__all_sync(0xffffffffu, tc::mbar_wait(full, parity))) return false;
-      tc::tc_fence_after();
-      const float f = pw[hsub * 132 + tile_len(c)];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        float x[16];
-        tc::tmem_ld16(src + 16 * j, x);
-        tc::tmem_wait_ld();
-#pragma unroll
-        for (int e = 0; e < 16; ++e) S[16 * j + e] = fmaf(f, S[16 * j + e], x[e]);
-      }
-      tc::tc_fence_before();
-      return true;
-    };
-    bool bad = false, bad_next = false;
-    if (kOut) publish();
-    bool ok = enter(0, &bad);
-    for (int c = 0; ok && c < nt; ++c) {
-      const int Lt = tile_len(c);
-      if constexpr (kOut) {
-        const bool want = c < nds;
-        if (!(ok = __all_sync(0xffffffffu, tc::mbar_wait(pv_done, c & 1)))) break;
-        uint4 lo[8];
-        if (want) {
-          const float f = r < Lt ? pwv[Lt - 1 - r] : 0.f;
-          if (bad) {         // the state takes the row as it came
-            const __nv_bfloat16* vr = v + (long long)(s0 + c * kPlTile + r) * H * D + hg * 128 + 64 * half;
-#pragma unroll 1
-            for (int i = 0; i < 8; ++i) sts16(chunk(c, L::kV, i), *reinterpret_cast<const uint4*>(vr + 8 * i));
-          }
-          uint4 x[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] = lds16(chunk(c, L::kV, i));
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            uint4 hi;
-            split_pair(x[i].x, f, &hi.x, &lo[i].x);
-            split_pair(x[i].y, f, &hi.y, &lo[i].y);
-            split_pair(x[i].z, f, &hi.z, &lo[i].z);
-            split_pair(x[i].w, f, &hi.w, &lo[i].w);
-            x[i] = hi;
-          }
-#pragma unroll
-          for (int i = 0; i < 8; ++i) sts16(chunk(c, L::kV, i), x[i]);
-          tc::fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive(v_hi);
-        }
-        if (c + 1 < nt && !(ok = enter(c + 1, &bad_next))) break;
-        if (want) {
-          if (!(ok = __all_sync(0xffffffffu, tc::mbar_wait(hi_done, c & 1)))) break;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) sts16(chunk(c, L::kV, i), lo[i]);
-          tc::fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive(v_lo);
-          // the products being done says that Q S of this tile has read the copy of S too
-          if (!(ok = join(c, ds_full, c & 1, ds_addr))) break;
-          if (c + 1 < nt) publish();
-        }
-        bad = bad_next;
-      } else {
-        const float f = r < Lt ? pwv[Lt - 1 - r] : 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint4 x = lds16(chunk(c, L::kV, i));
-          uint4 hi, lo;
-          split_pair(x.x, f, &hi.x, &lo.x);
-          split_pair(x.y, f, &hi.y, &lo.y);
-          split_pair(x.z, f, &hi.z, &lo.z);
-          split_pair(x.w, f, &hi.w, &lo.w);
-          sts16(chunk(c, L::kV, i), hi);
-          sts16(chunk(c, L::kQ, i), lo);
-        }
-        tc::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(c & 1 ? v_hi : kv_ok);
-        // the next tile's parts are written while this one is multiplied
-        if (c > 0 && !(ok = join(c - 1, ds_full + ((c - 1) & 1), ((c - 1) >> 1) & 1, ds_addr - 128 * ((c - 1) & 1)))) break;
-        if (c + 1 < nt) ok = enter(c + 1, &bad_next);
-      }
-    }
-    if (!kOut && ok)
-      ok = join(nt - 1, ds_full + ((nt - 1) & 1), ((nt - 1) >> 1) & 1, ds_addr - 128 * ((nt - 1) & 1));
-    if (ok && mine && s_dst) {
-#pragma unroll
-      for (int e = 0; e < 64; e += 4)
-        *reinterpret_cast<float4*>(s_dst + sc + e) = make_float4(S[e], S[e + 1], S[e + 2], S[e + 3]);
-    }
+    linear_state_role<D, kOut>(tc::smem_u32(smem), tmem, n_tok, nds, has_src | heads << 1);
   }
 
   tc::tc_fence_before();
@@ -734,7 +882,8 @@ linear_packed_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
 }
 
 // Between the two: the k-th sequence of several segments turns what each of
-// its segments but the last adds into the state that enters the next one.
+// its segments but the last adds (entry s + 1 for segment s) into the state
+// that enters segment s (entry s).
 // Four state values per thread.
 constexpr int kPlScanThreads = 256;
 
@@ -752,12 +901,13 @@ linear_packed_scan_kernel(const float* __restrict__ lambda, const int32_t* __res
     for (int i0 = 0; i0 < n_seqs; i0 += 32) {
       const int i = i0 + lane;
       int e = 0;
-      if (i < n_seqs && seq_ok(cu, i, tokens)) e = max(0, (cu[i + 1] - cu[i] + seg_tokens - 1) / seg_tokens - 1);
+      if (i < n_seqs && seq_ok(cu, i, tokens)) e = (cu[i + 1] - cu[i] + seg_tokens - 1) / seg_tokens;
+      if (e < 2) e = 0;
       const unsigned multi = __ballot_sync(0xffffffffu, e > 0);
       if (k < __popc(multi)) {
         const int w = __fns(multi, 0, k + 1);
         u.seq = i0 + w;
-        u.n_seg = __shfl_sync(0xffffffffu, e, w) + 1;
+        u.n_seg = __shfl_sync(0xffffffffu, e, w);
         int before = lane < w ? e : 0;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
@@ -782,6 +932,8 @@ linear_packed_scan_kernel(const float* __restrict__ lambda, const int32_t* __res
   float4 S = make_float4(0.f, 0.f, 0.f, 0.f);
   if (state_in && slot >= 0) S = *reinterpret_cast<const float4*>(state_in + slot * per + e);
   float* p = ws + u.ws * per + e;
+  *reinterpret_cast<float4*>(p) = S;           // state_out may be state_in: the outputs read it from here
+  p += per;
   const int n = u.n_seg - 1;
   for (int s0 = 0; s0 < n; s0 += 8) {          // eight sums in flight
     float4 x[8];
