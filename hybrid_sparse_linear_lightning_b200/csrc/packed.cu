@@ -129,9 +129,11 @@ sala_status run_dense(const sala_dense_desc* d, const void* q, const void* k, co
   // every sequence ends in a pair of tiles that may be part empty
   const int64_t pairs = (int64_t)d->tokens / (2 * Tt) + d->n_seqs;
   if (pairs * d->kv_heads > 0x7fffffffll) return SALA_ERR_UNSUPPORTED;
+  int kmax = 0;      // class of the longest sequence there can be, in key blocks
+  while ((int64_t)kPaBlock << (kmax + 1) <= (int64_t)d->tokens + kPaBlock - 1) ++kmax;
   kern<<<(unsigned)(pairs * d->kv_heads), kPaThreads, smem, st>>>(
       qm, km, vm, cu, static_cast<const bf16*>(v), static_cast<const bf16*>(gate),
-      static_cast<bf16*>(out), d->tokens, d->n_seqs, d->q_heads, d->kv_heads, Tt, sl2);
+      static_cast<bf16*>(out), d->tokens, d->n_seqs, d->q_heads, d->kv_heads, Tt, kmax, sl2);
   return launch_status();
 }
 
@@ -148,11 +150,26 @@ LinearPlan linear_plan(const sala_packed_linear_desc* d) {
   LinearPlan p;
   const int64_t groups = (d->heads + 128 / d->head_dim - 1) / (128 / d->head_dim);
   const int64_t tiles = ((int64_t)d->tokens + kPlTile - 1) / kPlTile * groups;
-  // four CTAs per SM by cutting; with many sequences only what one SM would
-  // take longer for than the whole card for all
-  int64_t seg = (tiles + 4 * kSms - 1) / (4 * kSms);
-  if (d->n_seqs * groups >= 2 * kSms) seg = std::max(seg, tiles / 128);
-  seg = std::min<int64_t>(std::max<int64_t>(seg, 4), 1 << 20);
+  // Tiles per segment: whole waves of CTAs over the card, taking the tokens for
+  // one sequence and three tiles' time for what a segment costs besides.  With
+  // sequences enough to fill the card twice, only what one SM would take longer
+  // for than the whole card for all is cut.
+  const int64_t per_head = ((int64_t)d->tokens + kPlTile - 1) / kPlTile;
+  int64_t seg = per_head;
+  if (d->n_seqs * groups < 2 * kSms) {
+    int64_t best = INT64_MAX;
+    for (int64_t n = 1; n <= 64; ++n) {
+      const int64_t len = (per_head + n - 1) / n;
+      const int64_t cost = (n * groups + kSms - 1) / kSms * (len + 3);
+      if (cost < best) {
+        best = cost;
+        seg = len;
+      }
+    }
+  } else {
+    seg = tiles / 128;
+  }
+  seg = std::min<int64_t>(std::max<int64_t>(seg, 8), 1 << 20);
   p.seg_tokens = (int)(seg * kPlTile);
   p.extra = d->tokens / p.seg_tokens;
   p.entries = p.extra + std::min<int64_t>(p.extra, d->n_seqs);

@@ -476,32 +476,39 @@ __device__ __forceinline__ bool seq_ok(const int32_t* cu, int i, int tokens) {
   return cu[i] >= 0 && cu[i] <= cu[i + 1] && cu[i + 1] <= tokens;
 }
 
-// Called by one warp: pair p of the packed sequences (pairs of tiles of 2 Tt
-// tokens, the last ones of a sequence first, which are the longest).
-__device__ __forceinline__ bool find_pair(const int32_t* cu, int n_seqs, int tokens, int Tt, int p,
-                                          int* seq, int* pair) {
+// Work of different lengths, longest first: a launch's last blocks are then
+// short ones, which keeps all SMs busy to its end.  Lengths are compared by
+// their power of two (class k: 2^k to 2^(k+1) - 1 units); count(i, k) says how
+// many pieces of class k sequence i has.  Called by one warp: piece p of all, as
+// a sequence, a class and a number among the sequence's pieces of that class.
+struct PackedPiece {
+  int seq, cls, idx;     // seq < 0: there are not so many
+};
+
+template <typename Count>
+__device__ __forceinline__ PackedPiece find_piece(int n_seqs, int kmax, int p, Count count) {
   const int lane = threadIdx.x & 31;
-  for (int i0 = 0; i0 < n_seqs; i0 += 32) {
-    const int i = i0 + lane;
-    int n = 0;
-    if (i < n_seqs && seq_ok(cu, i, tokens)) n = (cu[i + 1] - cu[i] + 2 * Tt - 1) / (2 * Tt);
-    int inc = n;
+  for (int k = kmax; k >= 0; --k)
+    for (int i0 = 0; i0 < n_seqs; i0 += 32) {
+      const int i = i0 + lane;
+      const int n = i < n_seqs ? count(i, k) : 0;
+      int inc = n;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += v;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += v;
+      }
+      const unsigned hit = __ballot_sync(0xffffffffu, p < inc);
+      if (hit) {
+        const int w = __ffs(hit) - 1;
+        return PackedPiece{i0 + w, k, p - __shfl_sync(0xffffffffu, inc - n, w)};
+      }
+      p -= __shfl_sync(0xffffffffu, inc, 31);
     }
-    const unsigned hit = __ballot_sync(0xffffffffu, p < inc);
-    if (hit) {
-      const int w = __ffs(hit) - 1;
-      *seq = i0 + w;
-      *pair = __shfl_sync(0xffffffffu, inc, w) - 1 - p;
-      return true;
-    }
-    p -= __shfl_sync(0xffffffffu, inc, 31);
-  }
-  return false;
+  return PackedPiece{-1, 0, 0};
 }
+
+__device__ __forceinline__ int length_class(int n) { return 31 - __clz(max(n, 1)); }
 
 template <int D>
 __global__ void __launch_bounds__(kPaThreads, 1)
@@ -509,7 +516,7 @@ dense_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
                   const __grid_constant__ CUtensorMap vmap, const int32_t* __restrict__ cu,
                   const __nv_bfloat16* __restrict__ v, const __nv_bfloat16* __restrict__ gate,
                   __nv_bfloat16* __restrict__ out, int tokens, int n_seqs, int Hq, int Hkv, int Tt,
-                  float sl2) {
+                  int kmax, float sl2) {
   extern __shared__ __align__(1024) uint8_t smem_pa[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_pa) + 1023) & ~uintptr_t(1023));
   PaJob* slot = reinterpret_cast<PaJob*>(smem + PaLayout<D>::kMisc + 16);
@@ -519,9 +526,21 @@ dense_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
       if (!seq_ok(cu, i, tokens)) set_status(kStatusBounds);
   if (threadIdx.x < 32) {
     PaJob job = {};
-    int s = 0, pair = 0;
-    if (find_pair(cu, n_seqs, tokens, Tt, blockIdx.x / Hkv, &s, &pair)) {
-      const int n = cu[s + 1] - cu[s];
+    // pair j of a sequence's tiles sees the keys up to its last token: pairs of
+    // class k or above begin where (2 j + 2) Tt exceeds 128 (2^k - 1) keys
+    const auto below = [&](int n, int k) {       // pairs of a sequence of n tokens below class k
+      const int pairs = (n + 2 * Tt - 1) / (2 * Tt);
+      const long long keys = ((1ll << k) - 1) * kPaBlock;
+      return n <= keys ? pairs : (int)min((long long)pairs, keys / (2 * Tt));
+    };
+    const PackedPiece w = find_piece(n_seqs, kmax, blockIdx.x / Hkv, [&](int i, int k) {
+      if (!seq_ok(cu, i, tokens)) return 0;
+      const int n = cu[i + 1] - cu[i];
+      return below(n, k + 1) - below(n, k);
+    });
+    if (w.seq >= 0) {
+      const int s = w.seq, n = cu[s + 1] - cu[s];
+      const int pair = below(n, w.cls + 1) - 1 - w.idx;
       job.live = 1;
       job.g = blockIdx.x % Hkv;
       job.krow = cu[s];

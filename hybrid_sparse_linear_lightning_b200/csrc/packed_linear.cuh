@@ -116,39 +116,42 @@ struct PlUnit {
   int ws;            // where the sequence's segment states begin (none where it has one segment)
 };
 
-// Called by one warp.
+__device__ __forceinline__ int segments_of(int n, int seg_tokens) {
+  return max(1, (n + seg_tokens - 1) / seg_tokens);
+}
+
+// Called by one warp: index p among all segments (longest first), or among all
+// but each sequence's last, which are whole.
 __device__ __forceinline__ PlUnit find_segment(const int32_t* cu, int n_seqs, int tokens, int seg_tokens,
                                                bool all, int p) {
-  const int lane = threadIdx.x & 31;
-  int ws = 0;
-  for (int i0 = 0; i0 < n_seqs; i0 += 32) {
-    const int i = i0 + lane;
-    int n = 0;
-    if (i < n_seqs && seq_ok(cu, i, tokens)) n = max(1, (cu[i + 1] - cu[i] + seg_tokens - 1) / seg_tokens);
-    const int e = n > 1 ? n : 0, own = all ? n : max(n - 1, 0);
-    int inc = own, ince = e;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int a = __shfl_up_sync(0xffffffffu, inc, o), b = __shfl_up_sync(0xffffffffu, ince, o);
-      if (lane >= o) {
-        inc += a;
-        ince += b;
+  const int kseg = length_class(seg_tokens / kPlTile);
+  const PackedPiece w = find_piece(n_seqs, all ? kseg : 0, p, [&](int i, int k) {
+    if (!seq_ok(cu, i, tokens)) return 0;
+    const int n = cu[i + 1] - cu[i];
+    if (!all) return segments_of(n, seg_tokens) - 1;
+    const int whole = n / seg_tokens, rest = n - whole * seg_tokens;
+    const bool has_rest = rest > 0 || n == 0;
+    return (k == kseg ? whole : 0) + (has_rest && k == length_class((rest + kPlTile - 1) / kPlTile));
+  });
+  PlUnit u = {w.seq, 0, 0, 0};
+  if (w.seq < 0) return u;
+  const int n = cu[w.seq + 1] - cu[w.seq];
+  u.n_seg = segments_of(n, seg_tokens);
+  // the rest of a sequence comes behind its whole segments, alone in its class
+  // where that is another one
+  u.seg = !all || w.cls == kseg ? w.idx : u.n_seg - 1;
+  if (u.n_seg > 1) {
+    int before = 0;
+    for (int i = threadIdx.x & 31; i < w.seq; i += 32)
+      if (seq_ok(cu, i, tokens)) {
+        const int e = segments_of(cu[i + 1] - cu[i], seg_tokens);
+        if (e > 1) before += e;
       }
-    }
-    const unsigned hit = __ballot_sync(0xffffffffu, p < inc);
-    if (hit) {
-      const int w = __ffs(hit) - 1;
-      PlUnit u;
-      u.seq = i0 + w;
-      u.n_seg = __shfl_sync(0xffffffffu, n, w);
-      u.seg = p - __shfl_sync(0xffffffffu, inc - own, w);
-      u.ws = ws + __shfl_sync(0xffffffffu, ince - e, w);
-      return u;
-    }
-    p -= __shfl_sync(0xffffffffu, inc, 31);
-    ws += __shfl_sync(0xffffffffu, ince, 31);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
+    u.ws = before;
   }
-  return PlUnit{-1, 0, 0, 0};
+  return u;
 }
 
 // A load that stays where it is written: the compiler would else move it to
@@ -207,7 +210,8 @@ __device__ __forceinline__ void split_pair(uint32_t w, float f, uint32_t* hi, ui
   const float2 x = __fmul2_rn(__bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w)), make_float2(f, f));
   const __nv_bfloat162 h = __floats2bfloat162_rn(x.x, x.y);
   const float2 hf = __bfloat1622float2(h);
-  const __nv_bfloat162 l = __floats2bfloat162_rn(x.x - hf.x, x.y - hf.y);
+  const float2 d = __fadd2_rn(x, make_float2(-hf.x, -hf.y));
+  const __nv_bfloat162 l = __floats2bfloat162_rn(d.x, d.y);
   *hi = *reinterpret_cast<const uint32_t*>(&h);
   *lo = *reinterpret_cast<const uint32_t*>(&l);
 }
@@ -249,19 +253,22 @@ __device__ __noinline__ void linear_state_role(uint32_t o_smem, uint32_t tmem, i
         sts16(chunk(c, L::kK, i), make_uint4(0, 0, 0, 0));
       }
     } else if (kOut) {
-      uint32_t acc = 0;
-#pragma unroll 1
+      __nv_bfloat162 top = __float2bfloat162_rn(0.f);       // largest magnitudes, NaN above all
+#pragma unroll
       for (int i0 = 0; i0 < 8; i0 += 4) {
         uint4 x[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) x[i] = lds16(chunk(c, L::kV, i0 + i));
+        for (int i = 0; i < 4; ++i) x[i] = lds16(chunk(c, L::kV, i0 + i));
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {      // an exponent of ones carries into bit 15 of its half
-        acc |= ((x[i].x & 0x7f807f80u) + 0x00800080u) | ((x[i].y & 0x7f807f80u) + 0x00800080u);
-        acc |= ((x[i].z & 0x7f807f80u) + 0x00800080u) | ((x[i].w & 0x7f807f80u) + 0x00800080u);
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            top = __hmax2_nan(top, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[e])));
+        }
       }
-      }
-      *bad = (acc & 0x80008000u) != 0;
+      const uint32_t tw = *reinterpret_cast<const uint32_t*>(&top);
+      *bad = (tw & 0x7f80u) == 0x7f80u || (tw & 0x7f800000u) == 0x7f800000u;
       if (*bad) {
 #pragma unroll 1
         for (int i = 0; i < 8; ++i) {
