@@ -7,12 +7,15 @@ import re
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libsala.so")
+CALLS = os.path.join(PKG, "_packed.so")           # Python module of the packed-batch calls, on libsala.so
+CALLS_SOURCE = os.path.join(CSRC, "packed_calls.cpp")
 SOURCES = ["api.cu", "packed.cu"]
 
 NVCC_FLAGS = [
@@ -35,9 +38,9 @@ def nvcc_path() -> str:
 
 
 def needs_build() -> bool:
-    if not os.path.exists(LIB):
+    if not (os.path.exists(LIB) and os.path.exists(CALLS)):
         return True
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(CALLS))
     deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(ROOT, "include", "sala.h")]
     return any(os.path.getmtime(p) > t for p in deps if os.path.isfile(p))
 
@@ -78,6 +81,19 @@ def check_register_splits(regs: dict, splits: dict = REGISTER_SPLIT_KERNELS) -> 
                                f"thread; its register split needs exactly {want}")
 
 
+def calls_command(out: str) -> list:
+    """Compile and link the Python module against torch's headers and libraries."""
+    import torch
+    at = os.path.dirname(torch.__file__)
+    inc = [os.path.join(at, "include"), os.path.join(at, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(nvcc_path())), "include")]
+    lib = os.path.join(at, "lib")
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-fvisibility=hidden",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *["-isystem" + i for i in inc],
+            "-o", out, CALLS_SOURCE, LIB + ".tmp", "-L" + lib, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+            "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + lib]
+
+
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     if not force and not needs_build():
         return LIB
@@ -101,7 +117,8 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
 
     with ThreadPoolExecutor(len(SOURCES)) as pool:   # one nvcc per source, side by side
         text = "".join(pool.map(compile_one, zip(SOURCES, objs)))
-    run([nvcc_path(), *NVCC_FLAGS, *LINK_FLAGS, "-o", LIB + ".tmp", *objs])
+    run([nvcc_path(), *NVCC_FLAGS, *LINK_FLAGS, "-Xlinker", "-soname,libsala.so", "-o", LIB + ".tmp", *objs])
+    run(calls_command(CALLS + ".tmp"))
     cur = ""
     for line in text.splitlines():
         m = re.search(r"Function properties for (\S+)", line)
@@ -115,6 +132,7 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     with open(REPORT, "w") as f:
         json.dump({"registers_per_thread": regs}, f, indent=1, sort_keys=True)
     os.replace(LIB + ".tmp", LIB)
+    os.replace(CALLS + ".tmp", CALLS)
     return LIB
 
 

@@ -159,6 +159,8 @@ def _load():
 
 LIB = _load()
 
+from . import _packed  # noqa: E402  (after libsala.so, which it is linked against)
+
 
 def status_string(s: int) -> str:
     return LIB.sala_status_string(int(s)).decode()
@@ -376,115 +378,32 @@ def sparse_prefill(q_norm, k_norm, v, gate, idx, *, block=64, topk=16, n_init=1,
 
 # ---------------------------------------------------------------------------- packed batches
 
-def _expect(name: str, t: torch.Tensor, shape, dtype, device):
-    """The helpers below check what the C entry points cannot see: a tensor's shape, type and device."""
-    if t.shape != shape:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.dtype is not dtype:
-        raise ValueError(f"{name}: {t.dtype}, expected {dtype}")
-    if t.device != device:
-        raise ValueError(f"{name}: on {t.device}, expected {device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: must be contiguous")
+# Below their signatures these helpers are csrc/packed_calls.cpp: they check what the C entry points
+# cannot see (a tensor's shape, type and device), work on the tensors' own device and its current
+# stream unless one is given, take outputs and workspaces from torch's allocator where none are given,
+# and return the sala_status of a refused call.
 
-
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-
-
-def _packed_call(what: str, device, fn, desc, tensors, ws, stream):
-    """Launch on the tensors' own device, on its current stream unless one is given.  ``ws``: None for
-    a call that takes no workspace, else (tensor or None, bytes needed)."""
-    if device.type != "cuda":
-        raise ValueError(f"{what}: tensors must be on a CUDA device")
-    if device.index != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            return _packed_call(what, device, fn, desc, tensors, ws, stream)
-    args = [None if t is None else t.data_ptr() for t in tensors]
-    if ws is not None:
-        t, need = ws
-        if t is None and need > 0:
-            t = _empty(need, torch.uint8, device, stream)
-        elif t is not None and (t.device != device or not t.is_contiguous()):
-            raise ValueError("ws: a contiguous tensor on the call's device")
-        args += [None, 0] if t is None else [t.data_ptr(), t.numel() * t.element_size()]
-    if stream is not None:
-        raw = stream.cuda_stream
-    elif _raw_stream is not None:
-        raw = _raw_stream(device.index)
-    else:
-        raw = torch.cuda.current_stream(device).cuda_stream
-    status = fn(ctypes.byref(desc), *args, raw)
-    if status != SALA_OK:
-        raise SalaError(status, what)
-
-
-def _empty(shape, dtype, device, stream):
-    """Memory that is reused in the order of the stream it was used on."""
+def _packed_call(what: str, stream, *args):
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
-
-
-def _out(out, shape, dtype, device, stream):
-    if out is None:
-        return _empty(shape, dtype, device, stream)
-    _expect("out", out, shape, dtype, device)
-    return out
+        r = getattr(_packed, what)(*args)
+    else:
+        with torch.cuda.stream(stream):      # memory is reused in the order of the stream it was used on
+            r = getattr(_packed, what)(*args)
+    if type(r) is int:
+        raise SalaError(r, "sala_" + what)
+    return r
 
 
 def qk_norm(q, k, wq, wk, positions=None, *, rope_base=10000.0, rms_eps=1e-6, outs=None, stream=None):
     """QK-RMSNorm of packed tokens q [T, Hq, d], k [T, Hk, d]; RoPE at ``positions`` [T] int32 where
     given.  Returns (q_norm, k_norm), bf16."""
-    T, Hq, D = q.shape
-    Hk, dev = k.shape[1], q.device
-    _expect("q", q, (T, Hq, D), q.dtype, dev)
-    _expect("k", k, (T, Hk, D), q.dtype, dev)
-    _expect("wq", wq, (D,), torch.float32, dev)
-    _expect("wk", wk, (D,), torch.float32, dev)
-    if positions is not None:
-        _expect("positions", positions, (T,), torch.int32, dev)
-    if outs is None:
-        outs = (_out(None, (T, Hq, D), torch.bfloat16, dev, stream),
-                _out(None, (T, Hk, D), torch.bfloat16, dev, stream))
-    else:
-        _expect("q_norm", outs[0], (T, Hq, D), torch.bfloat16, dev)
-        _expect("k_norm", outs[1], (T, Hk, D), torch.bfloat16, dev)
-    d = QkNormDesc(T, Hq, Hk, D, dtype_code(q.dtype), rope_base, rms_eps)
-    _packed_call("sala_qk_norm", dev, LIB.sala_qk_norm, d, (q, k, wq, wk, positions, *outs), None, stream)
-    return outs
+    return _packed_call("qk_norm", stream, q, k, wq, wk, positions, rope_base, rms_eps, outs)
 
 
 def dense_prefill(q_norm, k_norm, v, gate, cu_seqlens, *, scale=0.0, out=None, ws=None, stream=None):
     """Causal attention over packed prompts: q_norm, gate [T, Hq, d], k_norm, v [T, Hkv, d] bf16,
     cu_seqlens [n + 1] int32.  Returns out [T, Hq, d]; rows of no sequence are not written."""
-    T, Hq, D = q_norm.shape
-    Hkv, dev, n = k_norm.shape[1], q_norm.device, cu_seqlens.numel() - 1
-    for name, t, h in (("q_norm", q_norm, Hq), ("k_norm", k_norm, Hkv), ("v", v, Hkv), ("gate", gate, Hq)):
-        _expect(name, t, (T, h, D), torch.bfloat16, dev)
-    _expect("cu_seqlens", cu_seqlens, (n + 1,), torch.int32, dev)
-    out = _out(out, (T, Hq, D), torch.bfloat16, dev, stream)
-    d = DenseDesc(T, n, Hq, Hkv, D, SALA_BF16, scale)
-    need = int(LIB.sala_dense_workspace_size(ctypes.byref(d)))
-    _packed_call("sala_dense_prefill", dev, LIB.sala_dense_prefill, d,
-                 (q_norm, k_norm, v, gate, cu_seqlens, out), (ws, need), stream)
-    return out
-
-
-def _packed_linear(q_norm, k_norm, v, gate, lam, slots, n, pools):
-    T, H, D = q_norm.shape
-    dev = q_norm.device
-    for name, t, dt in (("q_norm", q_norm, torch.bfloat16), ("k_norm", k_norm, torch.bfloat16),
-                        ("v", v, v.dtype), ("gate", gate, v.dtype)):
-        _expect(name, t, (T, H, D), dt, dev)
-    _expect("lam", lam, (H,), torch.float32, dev)
-    if slots is not None:
-        _expect("slots", slots, (n,), torch.int32, dev)
-    n_slots = next((p.shape[0] for p in pools if p is not None), n)
-    for p in pools:
-        if p is not None:
-            _expect("state", p, (n_slots, H, D, D), torch.float32, dev)
-    return PackedLinearDesc(T, n, n_slots, H, D, dtype_code(v.dtype), 1.0)
+    return _packed_call("dense_prefill", stream, q_norm, k_norm, v, gate, cu_seqlens, scale, out, ws)
 
 
 def linear_packed_prefill(q_norm, k_norm, v, gate, lam, cu_seqlens, *, slots=None, state_in=None,
@@ -492,28 +411,15 @@ def linear_packed_prefill(q_norm, k_norm, v, gate, lam, cu_seqlens, *, slots=Non
     """Linear layer over packed prompts ([T, H, d] bf16); state pools [n_slots, H, d, d] fp32 (state_out
     may be state_in).  Without pools the slots (if any) index n entries.  Returns out; rows of no
     sequence are not written."""
-    n = cu_seqlens.numel() - 1
-    _expect("cu_seqlens", cu_seqlens, (n + 1,), torch.int32, q_norm.device)
-    d = _packed_linear(q_norm, k_norm, v, gate, lam, slots, n, (state_in, state_out))
-    d.scale = scale
-    out = _out(out, q_norm.shape, v.dtype, q_norm.device, stream)
-    need = int(LIB.sala_linear_packed_workspace_size(ctypes.byref(d)))
-    _packed_call("sala_linear_packed_prefill", q_norm.device, LIB.sala_linear_packed_prefill, d,
-                 (q_norm, k_norm, v, gate, lam, cu_seqlens, slots, state_in, state_out, out),
-                 (ws, need), stream)
-    return out
+    return _packed_call("linear_packed_prefill", stream, q_norm, k_norm, v, gate, lam, cu_seqlens, slots,
+                        state_in, state_out, scale, out, ws)
 
 
 def linear_packed_step(q_norm, k_norm, v, gate, lam, state, *, slots=None, scale=1.0, out=None,
                        stream=None):
     """One token of each request ([n, H, d]) through a linear layer; ``state`` [n_slots, H, d, d] fp32 is
     updated in place.  Returns out."""
-    d = _packed_linear(q_norm, k_norm, v, gate, lam, slots, q_norm.shape[0], (state,))
-    d.scale = scale
-    out = _out(out, q_norm.shape, v.dtype, q_norm.device, stream)
-    _packed_call("sala_linear_packed_step", q_norm.device, LIB.sala_linear_packed_step, d,
-                 (q_norm, k_norm, v, gate, lam, slots, state, out), None, stream)
-    return out
+    return _packed_call("linear_packed_step", stream, q_norm, k_norm, v, gate, lam, state, slots, scale, out)
 
 
 def prefix_decode(q_norm, k_norm, v, gate, prefix_k, prefix_v, k_cache, v_cache, lens, *, slots=None,
@@ -522,31 +428,8 @@ def prefix_decode(q_norm, k_norm, v, gate, prefix_k, prefix_v, k_cache, v_cache,
     v [B, Hkv, d], prefix_k, prefix_v [P, Hkv, d] (None for no prefix), k_cache, v_cache
     [n_slots, capacity, Hkv, d] bf16, lens [B] int32.  Appends the token to the caches (the caller
     advances ``lens``) and returns out [B, Hq, d]."""
-    B, Hq, D = q_norm.shape
-    Hkv, dev, bf = k_norm.shape[1], q_norm.device, torch.bfloat16
-    for name, t, h in (("q_norm", q_norm, Hq), ("k_norm", k_norm, Hkv), ("v", v, Hkv), ("gate", gate, Hq)):
-        _expect(name, t, (B, h, D), bf, dev)
-    if (prefix_k is None) != (prefix_v is None):
-        raise ValueError("prefix_k and prefix_v: both or neither")
-    P = 0 if prefix_k is None else prefix_k.shape[0]
-    if P == 0:
-        prefix_k = prefix_v = None
-    else:
-        _expect("prefix_k", prefix_k, (P, Hkv, D), bf, dev)
-        _expect("prefix_v", prefix_v, (P, Hkv, D), bf, dev)
-    n_slots, cap = k_cache.shape[:2]
-    _expect("k_cache", k_cache, (n_slots, cap, Hkv, D), bf, dev)
-    _expect("v_cache", v_cache, (n_slots, cap, Hkv, D), bf, dev)
-    _expect("lens", lens, (B,), torch.int32, dev)
-    if slots is not None:
-        _expect("slots", slots, (B,), torch.int32, dev)
-    out = _out(out, (B, Hq, D), bf, dev, stream)
-    d = PrefixDesc(B, P, n_slots, Hq, Hkv, D, cap, SALA_BF16, scale)
-    need = int(LIB.sala_prefix_workspace_size(ctypes.byref(d)))
-    _packed_call("sala_prefix_decode", dev, LIB.sala_prefix_decode, d,
-                 (q_norm, k_norm, v, gate, prefix_k, prefix_v, k_cache, v_cache, lens, slots, out),
-                 (ws, need), stream)
-    return out
+    return _packed_call("prefix_decode", stream, q_norm, k_norm, v, gate, prefix_k, prefix_v, k_cache, v_cache,
+                        lens, slots, scale, out, ws)
 
 
 def make_decode_io(layers: Sequence, outs: Sequence, states: Sequence, lams: Sequence,
