@@ -289,11 +289,11 @@ sala_status run_prefix(const sala_prefix_desc* d, const void* q, const void* k, 
     if (s != SALA_OK) return s;
   }
   // clusters grow until their CTAs fill the card twice over (two CTAs live on an
-  // SM), as long as every warp still has keys of a full cache
+  // SM), as long as every warp has eight steps of a full cache
   const int mtiles = (G + 15) / 16;
   const int64_t units = (int64_t)d->batch * d->kv_heads * mtiles;
   int cs = 1;
-  while (cs < kOwnMaxCluster && units * cs < 4 * 148 && d->cache_capacity > (int64_t)cs * kOwnWarps * 16) cs *= 2;
+  while (cs < kOwnMaxCluster && units * cs < 4 * 148 && d->cache_capacity > (int64_t)cs * kOwnWarps * 16 * 8) cs *= 2;
   if (units * cs > 0x7fffffffll) return SALA_ERR_UNSUPPORTED;
   auto kern = own_attn_kernel<D>;
   const size_t smem = OwnLayout<D>::kBytes;

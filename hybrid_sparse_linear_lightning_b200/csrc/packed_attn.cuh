@@ -43,7 +43,7 @@ constexpr int kPaBlock = 128;                // keys per block
 constexpr int kPaRegsLow = 80, kPaRegsHigh = 208;
 constexpr float kPaRescale = 8.0f;           // log2 units
 constexpr float kPaLowest = -3.402823466e38f;
-constexpr int kPaPolyPairsPer8 = 2;          // exponential pairs evaluated on the FMA pipe
+constexpr int kPaPolyPairsPer8 = 0;          // exponential pairs evaluated on the FMA pipe
 
 template <int D>
 struct PaLayout {
@@ -52,8 +52,8 @@ struct PaLayout {
   static constexpr int kSlots = D == 128 ? 5 : 8;    // ring of K and V tiles
   static constexpr int kRing = 2 * kTile;
   static constexpr int kBar = kRing + kSlots * kTile;
-  // q_full, ring_full[], ring_empty[], s_full[2], p_full[2], v_ready[3], fix_full[3], fin
-  static constexpr int kNumBars = 1 + 2 * kSlots + 2 + 2 + 3 + 3 + 1;
+  // q_full, ring_full[], ring_empty[], s_full[2], p_half[2], p_full[2], v_ready[3], fix_full[3], fin
+  static constexpr int kNumBars = 1 + 2 * kSlots + 2 + 2 + 2 + 3 + 3 + 1;
   static constexpr int kMisc = kBar + 8 * kNumBars;  // TMEM address, flag
   static constexpr int kBytes = kMisc + 16 + 64;
   static constexpr int col_s(int t) { return 128 * t; }
@@ -92,6 +92,35 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, u
       " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(tc::smem_u32(dst)),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(tc::smem_u32(bar)), "r"(x), "r"(y), "r"(z)
       : "memory");
+}
+
+// 16 bytes of shared memory by its 32-bit address.
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+  uint4 u;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "r"(a) : "memory");
+  return u;
+}
+__device__ __forceinline__ void sts16(uint32_t a, const uint4& u) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(u.x), "r"(u.y), "r"(u.z), "r"(u.w) : "memory");
+}
+
+// sigmoid(g) o for eight values: o / (1 + 2^(-g log2 e)), rounded to bf16.
+__device__ __forceinline__ uint4 gate_pack(const uint4& g, const uint4& a, const uint4& b) {
+  const uint32_t gw[4] = {g.x, g.y, g.z, g.w}, ow[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  uint32_t r[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    constexpr float kL = -1.4426950408889634f;
+    const float2 z = __fmul2_rn(__bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&gw[e])), make_float2(kL, kL));
+    const float2 d = __fadd2_rn(make_float2(tc::ex2_approx(z.x), tc::ex2_approx(z.y)), make_float2(1.f, 1.f));
+    float2 q;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q.x) : "f"(d.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q.y) : "f"(d.y));
+    q = __fmul2_rn(q, make_float2(__uint_as_float(ow[2 * e]), __uint_as_float(ow[2 * e + 1])));
+    const __nv_bfloat162 h2 = __floats2bfloat162_rn(q.x, q.y);
+    r[e] = *reinterpret_cast<const uint32_t*>(&h2);
+  }
+  return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
 // Non-finite bf16 values among the 8 of u: bit i set for value i.
@@ -153,6 +182,31 @@ struct PaPrefix {
   float2* part_ml;     // [split, batch, Hq]: maximum (log2 units), sum
 };
 
+// What does not depend on the job, by warps 1 and 2, while warp 0 looks it up.
+template <int D>
+__device__ __forceinline__ void pa_setup(const CUtensorMap& qmap, const CUtensorMap& kmap, const CUtensorMap& vmap,
+                                         uint8_t* smem) {
+  using L = PaLayout<D>;
+  if (threadIdx.x == 32) {
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBar);
+    for (int i = 0; i < L::kNumBars; ++i) {
+      const int at = i - (1 + 2 * L::kSlots);       // p_half, p_full: the tile's four warps; v_ready: two warps
+      tc::mbar_init(bars + i, at >= 2 && at < 6 ? 4 : at >= 6 && at < 9 ? 2 : 1);
+    }
+    tc::fence_barrier_init();
+    tc::tma_prefetch(&qmap);
+    tc::tma_prefetch(&kmap);
+    tc::tma_prefetch(&vmap);
+    *reinterpret_cast<volatile int*>(smem + L::kMisc + 4) = 0;
+  }
+  if (threadIdx.x >= 64 && threadIdx.x < 96) {
+    tc::tmem_alloc(reinterpret_cast<uint32_t*>(smem + L::kMisc), 512);
+    tc::tmem_relinquish();
+  }
+  tc::tc_fence_before();
+}
+
+// Behind pa_setup and a barrier of the block.
 template <int D, bool kDense, typename Epi>
 __device__ __forceinline__ void pa_run(const CUtensorMap& qmap, const CUtensorMap& kmap,
                                        const CUtensorMap& vmap, uint8_t* smem, const PaJob& job,
@@ -163,7 +217,10 @@ __device__ __forceinline__ void pa_run(const CUtensorMap& qmap, const CUtensorMa
   uint64_t* ring_full = bars + 1;
   uint64_t* ring_empty = ring_full + L::kSlots;
   uint64_t* s_full = ring_empty + L::kSlots;   // [2]
-  uint64_t* p_full = s_full + 2;               // [2]
+  // P is published in two halves of 64 keys: the first is multiplied while the
+  // exponentials of the second are taken
+  uint64_t* p_half = s_full + 2;               // [2]
+  uint64_t* p_full = p_half + 2;               // [2]
   // block fix_from + k is published on v_ready[k]: two tiles hold at most 256
   // tokens, so their diagonal crosses at most three blocks
   uint64_t* v_ready = p_full + 2;
@@ -171,52 +228,26 @@ __device__ __forceinline__ void pa_run(const CUtensorMap& qmap, const CUtensorMa
   // ring barrier): those who go over it have not followed the ring's phases
   uint64_t* fix_full = v_ready + 3;
   uint64_t* fin = fix_full + 3;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMisc);
   volatile int* found = reinterpret_cast<volatile int*>(smem + L::kMisc + 4);
 
   // the same in all lanes, and known to be: branches on it are uniform
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int G = Hq / Hkv;
   const int nb = max(job.nb[0], job.nb[1]);
-
-  if (threadIdx.x == 0) {
-    tc::mbar_init(q_full, 1);
-    for (int s = 0; s < L::kSlots; ++s) {
-      tc::mbar_init(ring_full + s, 1);
-      tc::mbar_init(ring_empty + s, 1);
-    }
-    for (int t = 0; t < 2; ++t) {
-      tc::mbar_init(s_full + t, 1);
-      tc::mbar_init(p_full + t, 4);
-    }
-    for (int i = 0; i < 3; ++i) {
-      tc::mbar_init(v_ready + i, 2);
-      tc::mbar_init(fix_full + i, 1);
-    }
-    tc::mbar_init(fin, 1);
-    tc::fence_barrier_init();
-    *found = 0;
-    const uint32_t qb = (uint32_t)(G * Tt * 128 * L::kAtoms);
-    tc::mbar_expect_tx(q_full, job.ntok[1] > 0 ? 2 * qb : qb);
-    for (int t = 0; t < 2; ++t)
-      if (job.ntok[t] > 0)
-        for (int a = 0; a < L::kAtoms; ++a)
-          tma_load_3d(smem + t * L::kTile + a * 16384, &qmap, q_full, 64 * a, job.g * G, job.tok[t]);
-  }
-  if (warp == 2) {
-    tc::tmem_alloc(tmem_slot, 512);
-    tc::tmem_relinquish();
-  }
-  tc::tc_fence_before();
-  __syncthreads();
   tc::tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = *reinterpret_cast<uint32_t*>(smem + L::kMisc);
 
   if (warp < 4) {
     tc::setmaxnreg_dec<kPaRegsLow>();
     if (warp == 0) {
       // ------------------------------------------------------------ TMA producer
       if (tc::elect_one()) {
+        const uint32_t qb = (uint32_t)(G * Tt * 128 * L::kAtoms);
+        tc::mbar_expect_tx(q_full, job.ntok[1] > 0 ? 2 * qb : qb);
+        for (int t = 0; t < 2; ++t)
+          if (job.ntok[t] > 0)
+            for (int a = 0; a < L::kAtoms; ++a)
+              tma_load_3d(smem + t * L::kTile + a * 16384, &qmap, q_full, 64 * a, job.g * G, job.tok[t]);
         int m = 0;
         for (; m < 2 * nb; ++m) {       // K(0) V(0) K(1) V(1) ...
           const int st = m % L::kSlots, use = m / L::kSlots;
@@ -263,14 +294,14 @@ __device__ __forceinline__ void pa_run(const CUtensorMap& qmap, const CUtensorMa
           tc::mma_commit(s_full + t);
           release(t, j, 2 * j);
         };
-        auto issue_pv = [&](int t, int j) {
+        auto issue_pv = [&](int t, int j, int half) {
           const uint32_t v_addr = ring + ((2 * j + 1) % L::kSlots) * L::kTile;
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
+          for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
             tc::mma_bf16_ts(tmem + L::col_o(t), tmem + L::col_s(t) + kk * 8,
                             tc::smem_desc_sw128(v_addr + kk * 2048, 16384, 1024), idesc_o,
                             (j > 0 || kk > 0));
-          release(t, j, 2 * j + 1);
+          if (half) release(t, j, 2 * j + 1);
         };
         bool ok = tc::mbar_wait(q_full, 0) && wait_tile(0);
         if (ok) {
@@ -286,9 +317,12 @@ __device__ __forceinline__ void pa_run(const CUtensorMap& qmap, const CUtensorMa
           }
           for (int t = 0; ok && t < 2; ++t) {
             if (j >= job.nb[t]) continue;
+            if (!(ok = tc::mbar_wait(p_half + t, j & 1))) break;
+            tc::tc_fence_after();
+            issue_pv(t, j, 0);
             if (!(ok = tc::mbar_wait(p_full + t, j & 1))) break;
             tc::tc_fence_after();
-            issue_pv(t, j);
+            issue_pv(t, j, 1);
             if (j + 1 < job.nb[t]) {
               if (!(ok = wait_tile(2 * j + 2))) break;
               tc::tc_fence_after();
@@ -388,78 +422,89 @@ __device__ __forceinline__ void pa_run(const CUtensorMap& qmap, const CUtensorMa
           pk[e] = *reinterpret_cast<uint32_t*>(&h2);
         }
         tc::tmem_st16_u(s_addr + 16 * q0, pk);
+        if (q0 & 1) {
+          tc::tmem_wait_st();
+          tc::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive((q0 == 1 ? p_half : p_full) + t);
+        }
       }
       const float2 s01 = __fadd2_rn(__fadd2_rn(acc4[0], acc4[1]), __fadd2_rn(acc4[2], acc4[3]));
       // a NaN or infinite logit makes the row NaN: mx x 0 is NaN then, else 0
       l += s01.x + s01.y + mx * 0.f;
-      tc::tmem_wait_st();
-      tc::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(p_full + t);
     }
     asm volatile("bar.sync 1, 320;" ::: "memory");
+    // A thread holds a row; rows are D values apart or further.  64 columns at a
+    // time go through the ring (8 KB for each warp, no tile is needed any more), so
+    // that a row is read and written in pieces of 128 bytes or more.
     const long long head = job.g * G + (r - tt * G);
-    const long long row = (long long)(job.tok[t] + tt) * Hq + head;
-    if constexpr (kDense) {
-      uint4 graw[D / 8];
-      if (valid) {
-        const uint4* gp = reinterpret_cast<const uint4*>(epi.gate + row * D);
+    const long long row = valid ? (long long)(job.tok[t] + tt) * Hq + head : -1;
+    ok = __all_sync(0xffffffffu, ok && tc::mbar_wait(fin, 0));
+    if (ok && nbt > 0) {
+      tc::tc_fence_after();
+      const bool bad = kDense && *found;
+      // logits that are all -infinity leave no weights: 0 / 0
+      const float mul = !kDense ? 1.f : m == kPaLowest ? NAN : 1.f / l;
+      const long long part = kDense ? 0 : (long long)job.split * batch * Hq;
+      if constexpr (!kDense)
+        if (valid) epi.part_ml[part + row] = make_float2(m, l);
+      // 16-byte chunk x of a row of 64 fp32 lies at place (x >> 1 | (x & 1) << 3) ^ (row & 7)
+      // of its 16: free of bank conflicts by rows and by pairs of chunks
+      const uint32_t stg = tc::smem_u32(smem + L::kRing) + (warp - 4) * 8192;
+      const uint32_t put_a = stg + lane * 256 + ((lane & 7) << 4);
+      const int cr = lane >> 3, cq = lane & 7;          // row (+ 4 i) and 8-column chunk of a copy
+#pragma unroll 1
+      for (int c0 = 0; c0 < D; c0 += 64) {
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) graw[c] = gp[c];
-      }
-      ok = __all_sync(0xffffffffu, ok && tc::mbar_wait(fin, 0));
-      if (ok && nbt > 0) {
-        tc::tc_fence_after();
-        const bool bad = *found;
-        // logits that are all -infinity leave no weights: 0 / 0
-        const float inv_l = m == kPaLowest ? NAN : 1.f / l;
-#pragma unroll
-        for (int c0 = 0; c0 < D; c0 += 32) {
+        for (int h = 0; h < 2; ++h) {
           float o[32];
-          tc::tmem_ld32(o_addr + c0, o);
+          tc::tmem_ld32(o_addr + c0 + 32 * h, o);
           tc::tmem_wait_ld();
 #pragma unroll
-          for (int c = 0; c < 32; ++c) o[c] *= inv_l;
-          if (bad && valid) {
-            for (int u = job.fix_from * kPaBlock; u < lim; ++u) {
-              const __nv_bfloat16* vr = epi.v + ((long long)(job.krow + u) * Hkv + job.g) * D + c0;
+          for (int c = 0; c < 32; ++c) o[c] *= mul;
+          if constexpr (kDense) {
+            if (bad && valid) {
+              for (int u = job.fix_from * kPaBlock; u < lim; ++u) {
+                const __nv_bfloat16* vr = epi.v + ((long long)(job.krow + u) * Hkv + job.g) * D + c0 + 32 * h;
 #pragma unroll
-              for (int c = 0; c < 32; ++c) {
-                const float f = to_f32(vr[c]);
-                if (!isfinite(f)) o[c] += f;
+                for (int c = 0; c < 32; ++c) {
+                  const float f = to_f32(vr[c]);
+                  if (!isfinite(f)) o[c] += f;
+                }
               }
             }
           }
-          if (valid) {
 #pragma unroll
-            for (int c = 0; c < 32; c += 8) {
-              float gv[8];
-              load8(reinterpret_cast<const __nv_bfloat16*>(&graw[(c0 + c) / 8]), gv);
+          for (int x = 0; x < 8; ++x)
+            sts16(put_a ^ (((8 * h + x) >> 1 | (x & 1) << 3) << 4),
+                  make_uint4(__float_as_uint(o[4 * x]), __float_as_uint(o[4 * x + 1]), __float_as_uint(o[4 * x + 2]),
+                             __float_as_uint(o[4 * x + 3])));
+        }
+        __syncwarp();
+        long long at[8];
+        uint4 g[8];
 #pragma unroll
-              for (int e = 0; e < 8; ++e) gv[e] = sigmoidf_(gv[e]) * o[c + e];
-              store8(epi.out + row * D + c0 + c, gv);
+        for (int i = 0; i < 8; ++i) {
+          at[i] = __shfl_sync(0xffffffffu, row, cr + 4 * i);
+          if constexpr (kDense)
+            if (at[i] >= 0) g[i] = *reinterpret_cast<const uint4*>(epi.gate + at[i] * D + c0 + 8 * cq);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int rr = cr + 4 * i;
+          const uint32_t get_a = (stg + rr * 256 + ((rr & 7) << 4)) ^ (cq << 4);      // chunks 2 cq and 2 cq + 1
+          const uint4 x = lds16(get_a), y = lds16(get_a ^ 128);
+          if (at[i] >= 0) {
+            if constexpr (kDense) {
+              *reinterpret_cast<uint4*>(epi.out + at[i] * D + c0 + 8 * cq) = gate_pack(g[i], x, y);
+            } else {
+              uint4* dst = reinterpret_cast<uint4*>(epi.part_o + (part + at[i]) * D + c0 + 8 * cq);
+              dst[0] = x;
+              dst[1] = y;
             }
           }
         }
-      }
-    } else {
-      ok = __all_sync(0xffffffffu, ok && tc::mbar_wait(fin, 0));
-      if (ok && nbt > 0) {
-        tc::tc_fence_after();
-        const long long at = (long long)job.split * batch * Hq + row;
-        if (valid) epi.part_ml[at] = make_float2(m, l);
-#pragma unroll
-        for (int c0 = 0; c0 < D; c0 += 32) {
-          float o[32];
-          tc::tmem_ld32(o_addr + c0, o);
-          tc::tmem_wait_ld();
-          if (valid) {
-#pragma unroll
-            for (int c = 0; c < 32; c += 4)
-              *reinterpret_cast<float4*>(epi.part_o + at * D + c0 + c) =
-                  make_float4(o[c], o[c + 1], o[c + 2], o[c + 3]);
-          }
-        }
+        __syncwarp();
       }
     }
   }
@@ -524,6 +569,7 @@ dense_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
   if (blockIdx.x == 0)
     for (int i = threadIdx.x; i < n_seqs; i += kPaThreads)
       if (!seq_ok(cu, i, tokens)) set_status(kStatusBounds);
+  pa_setup<D>(qmap, kmap, vmap, smem);
   if (threadIdx.x < 32) {
     PaJob job = {};
     // pair j of a sequence's tiles sees the keys up to its last token: pairs of
@@ -558,7 +604,13 @@ dense_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
   }
   __syncthreads();
   const PaJob job = *slot;
-  if (!job.live) return;
+  if (!job.live) {
+    if (threadIdx.x >= 64 && threadIdx.x < 96) {
+      tc::tc_fence_after();
+      tc::tmem_dealloc(*reinterpret_cast<uint32_t*>(smem + PaLayout<D>::kMisc), 512);
+    }
+    return;
+  }
   pa_run<D, true>(qmap, kmap, vmap, smem, job, PaDense{v, gate, out}, 0, Hq, Hkv, Tt, sl2);
 }
 

@@ -111,6 +111,8 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
   extern __shared__ __align__(1024) uint8_t smem_pp[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_pp) + 1023) & ~uintptr_t(1023));
   pdl_launch();
+  pa_setup<D>(qmap, kmap, vmap, smem);
+  __syncthreads();
   PaJob job;
   job.live = 1;
   job.g = blockIdx.x % Hkv;

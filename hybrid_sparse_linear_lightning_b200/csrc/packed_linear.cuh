@@ -168,35 +168,6 @@ __device__ __forceinline__ void st_out(__nv_bfloat16* p, const uint4& u) {
                : "memory");
 }
 
-// 16 bytes of shared memory by its 32-bit address.
-__device__ __forceinline__ uint4 lds16(uint32_t a) {
-  uint4 u;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "r"(a) : "memory");
-  return u;
-}
-__device__ __forceinline__ void sts16(uint32_t a, const uint4& u) {
-  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(u.x), "r"(u.y), "r"(u.z), "r"(u.w) : "memory");
-}
-
-// sigmoid(g) o for eight values: o / (1 + 2^(-g log2 e)), rounded to bf16.
-__device__ __forceinline__ uint4 gate_pack(const uint4& g, const uint4& a, const uint4& b) {
-  const uint32_t gw[4] = {g.x, g.y, g.z, g.w}, ow[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-  uint32_t r[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    constexpr float kL = -1.4426950408889634f;
-    const float2 z = __fmul2_rn(__bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&gw[e])), make_float2(kL, kL));
-    const float2 d = __fadd2_rn(make_float2(tc::ex2_approx(z.x), tc::ex2_approx(z.y)), make_float2(1.f, 1.f));
-    float2 q;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q.x) : "f"(d.x));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q.y) : "f"(d.y));
-    q = __fmul2_rn(q, make_float2(__uint_as_float(ow[2 * e]), __uint_as_float(ow[2 * e + 1])));
-    const __nv_bfloat162 h2 = __floats2bfloat162_rn(q.x, q.y);
-    r[e] = *reinterpret_cast<const uint32_t*>(&h2);
-  }
-  return make_uint4(r[0], r[1], r[2], r[3]);
-}
-
 // 2D tiled store of one box.
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t src, int x, int y) {
   asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
@@ -656,7 +627,6 @@ linear_packed_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBar);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMisc);
   PlUnit* unit = reinterpret_cast<PlUnit*>(smem + L::kMisc + 8);
-  volatile int* found = reinterpret_cast<volatile int*>(smem + L::kMisc + 32);   // [2][8]
   float* pw = reinterpret_cast<float*>(smem + L::kPw);
 
   // the same in all lanes, and known to be: branches on it are uniform
