@@ -55,13 +55,13 @@ struct PlLayout {
   static constexpr int kBar = kPw + 2 * 132 * 4;
   // ld_full[2], ld_empty[2], kv_ok, qk_full, p_full, pv_done, o_full, o_empty, s_full, v_hi, v_lo,
   // hi_done, ds_full[2], fin, s_ld, e_sync, v_sync
-  static constexpr int kNumBars = 20;
+  static constexpr int kNumBars = 24;
   // Barriers by their byte offset.  Every barrier's phase is waited for by all who
   // wait on it before the next one can complete.  Where kOut is false, tiles of
   // even and odd number use kv_ok and v_hi (V' written) in turn for that.
   enum : uint32_t {
-    ld_full = 0,         // [2] Q, K, V of a tile have landed
-    ld_empty = 16,       // [2] products done, and outputs written
+    ld_full = 0,         // [2] K and V of a tile have landed
+    ld_empty = 16,       // [2] K^T V' is done
     kv_ok = 32,          // rows past the end and non-finite values are 0
     qk_full = 40,
     p_full = 48,
@@ -77,6 +77,8 @@ struct PlLayout {
     s_ld = 136,          // the entering state has landed
     e_sync = 144,        // among the warps that write outputs
     v_sync = 152,        // the leaving state lies in shared memory
+    q_full = 160,        // [2] Q has landed
+    q_empty = 176,       // [2] outputs are written
   };
   static constexpr int kMisc = kBar + 8 * kNumBars;        // TMEM address, unit, found[2][8]
   static constexpr int kShared = kMisc + 96;               // PlShared
@@ -152,6 +154,28 @@ __device__ __forceinline__ PlUnit find_segment(const int32_t* cu, int n_seqs, in
     u.ws = before;
   }
   return u;
+}
+
+// sigmoid(g) o for eight values, with the sigmoid of the linear layers:
+// 1/2 + tanh(g / 2) / 2 on the hardware's tanh (absolute error 2^-12), half the
+// special-function operations of an exponential and a reciprocal, which take
+// 4000 cycles of the 8000 that a tile's outputs have.
+__device__ __forceinline__ uint4 gate_pack_tanh(const uint4& g, const uint4& a, const uint4& b) {
+  const uint32_t gw[4] = {g.x, g.y, g.z, g.w}, ow[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  const float2 half2 = make_float2(0.5f, 0.5f);
+  uint32_t r[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float2 z = __fmul2_rn(__bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&gw[e])), half2);
+    float2 t;
+    asm("tanh.approx.f32 %0, %1;" : "=f"(t.x) : "f"(z.x));
+    asm("tanh.approx.f32 %0, %1;" : "=f"(t.y) : "f"(z.y));
+    const float2 q = __fmul2_rn(__ffma2_rn(t, half2, half2),
+                                make_float2(__uint_as_float(ow[2 * e]), __uint_as_float(ow[2 * e + 1])));
+    const __nv_bfloat162 h2 = __floats2bfloat162_rn(q.x, q.y);
+    r[e] = *reinterpret_cast<const uint32_t*>(&h2);
+  }
+  return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
 // A load that stays where it is written: the compiler would else move it to
@@ -574,7 +598,7 @@ __device__ __noinline__ void linear_output_role(uint32_t o_smem, uint32_t tmem, 
     };
     // the staged half: gated and written
     auto store = [&](int h) {
-      constexpr int kB = 4;            // rows of a thread at a time
+      constexpr int kB = 8;            // rows of a thread at a time
       __nv_bfloat16* p = out + at + 64 * h;
 #pragma unroll
       for (int i0 = 0; i0 < 8; i0 += kB) {
@@ -585,7 +609,7 @@ __device__ __noinline__ void linear_output_role(uint32_t o_smem, uint32_t tmem, 
           b[i] = lds16((get_a ^ 128) + (i0 + i) * 4096);
         }
 #pragma unroll
-        for (int i = 0; i < kB; ++i) a[i] = gate_pack(g[i0 + i], a[i], b[i]);
+        for (int i = 0; i < kB; ++i) a[i] = gate_pack_tanh(g[i0 + i], a[i], b[i]);
 #pragma unroll
         for (int i = 0; i < kB; ++i, p += 16 * rs)
           if (cr + 16 * (i0 + i) < Lt && 64 * h < cols) st_out(p, a[i]);
@@ -605,7 +629,7 @@ __device__ __noinline__ void linear_output_role(uint32_t o_smem, uint32_t tmem, 
       ok = sync();
     }
     if (!ok) break;
-    if (threadIdx.x == 256) tc::mbar_arrive(bar + L::ld_empty + 8 * (c & 1));
+    if (threadIdx.x == 256) tc::mbar_arrive(bar + L::q_empty + 8 * (c & 1));
   }
 }
 
@@ -670,7 +694,9 @@ linear_packed_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(bars + L::ld_full / 8 + i, 1);
-      tc::mbar_init(bars + L::ld_empty / 8 + i, kOut ? 2 : 1);     // products done, and outputs written
+      tc::mbar_init(bars + L::ld_empty / 8 + i, 1);
+      tc::mbar_init(bars + L::q_full / 8 + i, 1);
+      tc::mbar_init(bars + L::q_empty / 8 + i, 1);
       tc::mbar_init(bars + L::ds_full / 8 + i, 1);
     }
     PlShared* sh = reinterpret_cast<PlShared*>(smem + L::kShared);
@@ -711,7 +737,7 @@ linear_packed_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
     if (warp == 0) {
       // ------------------------------------------------------------ TMA producer
       if (tc::elect_one()) {
-        int c = 0;
+        int c = 0, q_tiles = 0;
         for (; c < nt; ++c) {
           const int st = c & 1, use = c >> 1;
           if (use > 0 && !tc::mbar_wait(bar + L::ld_empty + 8 * st, (use - 1) & 1)) break;
@@ -719,13 +745,23 @@ linear_packed_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
           // (the next one cannot be before tile 1 is here)
           if (c == 1 && has_src && !tc::mbar_wait(bar + L::s_full, 0)) break;
           const uint32_t stage = o_smem + st * L::kStage;
-          tc::mbar_expect_tx(bar + L::ld_full + 8 * st, kOut ? 98304 : 65536);
+          tc::mbar_expect_tx(bar + L::ld_full + 8 * st, 65536);
           for (int a = 0; a < 2; ++a) {
             const int x = hg * 128 + 64 * a, y = s0 + c * kPlTile;
             tc::tma_load_2d(stage + L::kK + a * 16384, &kmap, bar + L::ld_full + 8 * st, x, y);
-            if (kOut) tc::tma_load_2d(stage + L::kQ + a * 16384, &qmap, bar + L::ld_full + 8 * st, x, y);
             tc::tma_load_2d(stage + L::kV + a * 16384, &vmap, bar + L::ld_full + 8 * st, x, y);
             if (kOut) tc::tma_prefetch_l2_2d(&gmap, x, y);     // its loads come a tile later
+          }
+          if (kOut) {            // Q's place is the outputs' until they are written
+            if (use > 0 && !tc::mbar_wait(bar + L::q_empty + 8 * st, (use - 1) & 1)) {
+              ++c;
+              break;
+            }
+            tc::mbar_expect_tx(bar + L::q_full + 8 * st, 32768);
+            for (int a = 0; a < 2; ++a)
+              tc::tma_load_2d(stage + L::kQ + a * 16384, &qmap, bar + L::q_full + 8 * st, hg * 128 + 64 * a,
+                              s0 + c * kPlTile);
+            q_tiles = c + 1;
           }
           if (c == 0 && has_src) {
             const int row = u.n_seg > 1 ? ((u.ws + u.seg) * H + hg * NH) * D : own_row;
@@ -738,6 +774,7 @@ linear_packed_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
         if (has_src) tc::mbar_wait(bar + L::s_ld, 0);
         // no copy is in flight when this warp ends, whatever became of the others
         for (int i = max(0, c - 2); i < c; ++i) tc::mbar_wait(bar + L::ld_full + 8 * (i & 1), (i >> 1) & 1);
+        for (int i = max(0, q_tiles - 2); i < q_tiles; ++i) tc::mbar_wait(bar + L::q_full + 8 * (i & 1), (i >> 1) & 1);
       }
     } else if (warp == 1) {
       // ------------------------------------------------------------ MMA issuer
@@ -767,7 +804,8 @@ linear_packed_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
                             tc::smem_desc_sw128(w + kk * 2048, 16384, 1024), id_nn, acc || kk > 0);
         };
         auto loaded = [&](int c) {
-          return tc::mbar_wait(bar + L::ld_full + 8 * (c & 1), (c >> 1) & 1) && tc::mbar_wait(bar + L::kv_ok, c & 1);
+          return tc::mbar_wait(bar + L::ld_full + 8 * (c & 1), (c >> 1) & 1) && tc::mbar_wait(bar + L::kv_ok, c & 1) &&
+                 tc::mbar_wait(bar + L::q_full + 8 * (c & 1), (c >> 1) & 1);
         };
         bool ok = true;
         if constexpr (kOut) {
