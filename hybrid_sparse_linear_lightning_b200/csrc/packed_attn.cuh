@@ -40,7 +40,7 @@ namespace sala {
 
 constexpr int kPaThreads = 384;
 constexpr int kPaBlock = 128;                // keys per block
-constexpr int kPaRegsLow = 80, kPaRegsHigh = 208;
+constexpr int kPaRegsLow = 72, kPaRegsHigh = 216;
 constexpr float kPaRescale = 8.0f;           // log2 units
 constexpr float kPaLowest = -3.402823466e38f;
 constexpr int kPaPolyPairsPer8 = 0;          // exponential pairs evaluated on the FMA pipe
@@ -523,20 +523,26 @@ __device__ __forceinline__ bool seq_ok(const int32_t* cu, int i, int tokens) {
 
 // Work of different lengths, longest first: a launch's last blocks are then
 // short ones, which keeps all SMs busy to its end.  Lengths are compared by
-// their power of two (class k: 2^k to 2^(k+1) - 1 units); count(i, k) says how
-// many pieces of class k sequence i has.  Called by one warp: piece p of all, as
-// a sequence, a class and a number among the sequence's pieces of that class.
+// their power of two (class k: 2^k to 2^(k+1) - 1 units); count(n, k) says how
+// many pieces of class k a sequence of n tokens has.  Called by one warp: piece p
+// of all, as a sequence, a class and a number among the sequence's pieces of that
+// class.
 struct PackedPiece {
   int seq, cls, idx;     // seq < 0: there are not so many
 };
 
 template <typename Count>
-__device__ __forceinline__ PackedPiece find_piece(int n_seqs, int kmax, int p, Count count) {
+__device__ __forceinline__ PackedPiece find_piece(const int32_t* cu, int n_seqs, int tokens, int kmax, int p,
+                                                  Count count) {
   const int lane = threadIdx.x & 31;
+  auto length = [&](int i) { return i < n_seqs && seq_ok(cu, i, tokens) ? cu[i + 1] - cu[i] : -1; };
+  int len = length(lane);
+#pragma unroll 1
   for (int k = kmax; k >= 0; --k)
+#pragma unroll 1
     for (int i0 = 0; i0 < n_seqs; i0 += 32) {
-      const int i = i0 + lane;
-      const int n = i < n_seqs ? count(i, k) : 0;
+      if (n_seqs > 32) len = length(i0 + lane);
+      const int n = len >= 0 ? count(len, k) : 0;
       int inc = n;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -574,16 +580,13 @@ dense_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
     PaJob job = {};
     // pair j of a sequence's tiles sees the keys up to its last token: pairs of
     // class k or above begin where (2 j + 2) Tt exceeds 128 (2^k - 1) keys
-    const auto below = [&](int n, int k) {       // pairs of a sequence of n tokens below class k
-      const int pairs = (n + 2 * Tt - 1) / (2 * Tt);
-      const long long keys = ((1ll << k) - 1) * kPaBlock;
-      return n <= keys ? pairs : (int)min((long long)pairs, keys / (2 * Tt));
+    const uint32_t pair_tokens = 2 * Tt;
+    const auto below = [&](int n, int k) {       // pairs of a sequence of n tokens below class k (k <= 24)
+      const uint32_t keys = ((1u << k) - 1) * kPaBlock;
+      return (int)((uint32_t)n <= keys ? (n + pair_tokens - 1) / pair_tokens : keys / pair_tokens);
     };
-    const PackedPiece w = find_piece(n_seqs, kmax, blockIdx.x / Hkv, [&](int i, int k) {
-      if (!seq_ok(cu, i, tokens)) return 0;
-      const int n = cu[i + 1] - cu[i];
-      return below(n, k + 1) - below(n, k);
-    });
+    const PackedPiece w = find_piece(cu, n_seqs, tokens, kmax, blockIdx.x / Hkv,
+                                     [&](int n, int k) { return below(n, k + 1) - below(n, k); });
     if (w.seq >= 0) {
       const int s = w.seq, n = cu[s + 1] - cu[s];
       const int pair = below(n, w.cls + 1) - 1 - w.idx;

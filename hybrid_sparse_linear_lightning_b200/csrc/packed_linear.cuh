@@ -127,9 +127,7 @@ __device__ __forceinline__ int segments_of(int n, int seg_tokens) {
 __device__ __forceinline__ PlUnit find_segment(const int32_t* cu, int n_seqs, int tokens, int seg_tokens,
                                                bool all, int p) {
   const int kseg = length_class(seg_tokens / kPlTile);
-  const PackedPiece w = find_piece(n_seqs, all ? kseg : 0, p, [&](int i, int k) {
-    if (!seq_ok(cu, i, tokens)) return 0;
-    const int n = cu[i + 1] - cu[i];
+  const PackedPiece w = find_piece(cu, n_seqs, tokens, all ? kseg : 0, p, [&](int n, int k) {
     if (!all) return segments_of(n, seg_tokens) - 1;
     const int whole = n / seg_tokens, rest = n - whole * seg_tokens;
     const bool has_rest = rest > 0 || n == 0;
