@@ -141,7 +141,8 @@ sala_status run_dense(const sala_dense_desc* d, const void* q, const void* k, co
 struct LinearPlan {
   int seg_tokens;
   int64_t extra;        // most segments behind a sequence's first
-  int64_t entries;      // and with the first ones of these sequences
+  int64_t multi;        // most sequences of several segments
+  int64_t entries;      // states of theirs: before and behind each segment
   size_t total;         // workspace: the states that enter them
 };
 
@@ -152,8 +153,10 @@ LinearPlan linear_plan(const sala_packed_linear_desc* d) {
   const int64_t tiles = ((int64_t)d->tokens + kPlTile - 1) / kPlTile * groups;
   // Tiles per segment: whole waves of CTAs over the card, taking the tokens for
   // one sequence and three tiles' time for what a segment costs besides.  With
-  // sequences enough to fill the card twice, only what one SM would take longer
-  // for than the whole card for all is cut.
+  // sequences enough to fill the card twice, only what one SM would take more than
+  // twice the whole card's time for is cut: the sums of the segments read keys and
+  // values once more (13 prompts of up to 23 tiles at 32 heads: 191 us whole, 198
+  // cut at 17).
   const int64_t per_head = ((int64_t)d->tokens + kPlTile - 1) / kPlTile;
   int64_t seg = per_head;
   if (d->n_seqs * groups < 2 * kSms) {
@@ -167,12 +170,13 @@ LinearPlan linear_plan(const sala_packed_linear_desc* d) {
       }
     }
   } else {
-    seg = tiles / 128;
+    seg = tiles / 64;
   }
   seg = std::min<int64_t>(std::max<int64_t>(seg, 8), 1 << 20);
   p.seg_tokens = (int)(seg * kPlTile);
   p.extra = d->tokens / p.seg_tokens;
-  p.entries = p.extra + std::min<int64_t>(p.extra, d->n_seqs);
+  p.multi = std::min<int64_t>(p.extra, d->n_seqs);
+  p.entries = p.extra + 2 * p.multi;
   p.total = align_up((size_t)p.entries * d->heads * d->head_dim * d->head_dim * sizeof(float));
   return p;
 }
@@ -211,14 +215,14 @@ sala_status run_linear(const sala_packed_linear_desc* d, const void* q, const vo
     return launch_status();
   };
   if (p.extra > 0) {
-    sala_status s = launch(linear_packed_kernel<D, false>, p.extra * groups, &allowed[0]);
+    sala_status s = launch(linear_packed_kernel<D, false>, (p.extra + p.multi) * groups, &allowed[0]);
     if (s != SALA_OK) return s;
     const int64_t per = (int64_t)d->heads * D * D / 4;
     const dim3 grid((unsigned)((per + kPlScanThreads - 1) / kPlScanThreads),
-                    (unsigned)std::min<int64_t>(d->n_seqs, p.extra));
+                    (unsigned)p.multi);
     if (grid.y > 65535) return SALA_ERR_UNSUPPORTED;
     linear_packed_scan_kernel<D><<<grid, kPlScanThreads, 0, st>>>(
-        lambda, cu, slots, state_in, ws, d->tokens, d->n_seqs, d->n_slots, d->heads, p.seg_tokens);
+        lambda, cu, slots, state_in, state_out, ws, d->tokens, d->n_seqs, d->n_slots, d->heads, p.seg_tokens);
     s = launch_status();
     if (s != SALA_OK) return s;
   }

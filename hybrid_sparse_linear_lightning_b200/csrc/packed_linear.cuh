@@ -13,12 +13,14 @@
 //
 // A sequence is cut into segments of whole tiles; a CTA walks one segment of
 // one head (two heads where d = 64, side by side in 128 columns).  Sequences
-// of several segments take three launches: the states that each segment but
-// the last adds (kOut = false), a scan over them, and the outputs.
+// of several segments take three launches: what each segment adds to the state
+// (kOut = false), a scan over them, which also gives the leaving state, and the
+// outputs.
 //
-// Rounding.  States are fp32: V' is split into two bf16 parts (hi + lo, 2^-16),
-// each tile's K^T V' is summed from zero on the tensor core and joined to S in
-// registers, so the tensor core's own rounding never adds up over tiles.  P
+// Rounding.  States are fp32: V' is split into three bf16 parts (24 bits; two,
+// 16 bits, where the state does not leave), each tile's K^T V' is summed from
+// zero on the tensor core and joined to S in registers, so the tensor core's own
+// rounding never adds up over tiles.  P
 // and the copy of S that Q multiplies are rounded to bf16; Q, K and V enter as
 // they are.
 //
@@ -55,7 +57,7 @@ struct PlLayout {
   static constexpr int kBar = kPw + 2 * 132 * 4;
   // ld_full[2], ld_empty[2], kv_ok, qk_full, p_full, pv_done, o_full, o_empty, s_full, v_hi, v_lo,
   // hi_done, ds_full[2], fin, s_ld, e_sync, v_sync
-  static constexpr int kNumBars = 24;
+  static constexpr int kNumBars = 26;
   // Barriers by their byte offset.  Every barrier's phase is waited for by all who
   // wait on it before the next one can complete.  Where kOut is false, tiles of
   // even and odd number use kv_ok and v_hi (V' written) in turn for that.
@@ -79,6 +81,8 @@ struct PlLayout {
     v_sync = 152,        // the leaving state lies in shared memory
     q_full = 160,        // [2] Q has landed
     q_empty = 176,       // [2] outputs are written
+    v_low = 192,         // the third part of V'
+    lo_done = 200,
   };
   static constexpr int kMisc = kBar + 8 * kNumBars;        // TMEM address, unit, found[2][8]
   static constexpr int kShared = kMisc + 96;               // PlShared
@@ -115,20 +119,21 @@ static_assert(sizeof(PlShared) <= 64, "its place in shared memory");
 struct PlUnit {
   int seq, seg;      // sequence, segment in it; seq < 0: none
   int n_seg;         // segments of the sequence
-  int ws;            // where the sequence's segment states begin (none where it has one segment)
+  int ws;            // where its n_seg + 1 states in the workspace begin (none where n_seg is 1)
 };
 
 __device__ __forceinline__ int segments_of(int n, int seg_tokens) {
   return max(1, (n + seg_tokens - 1) / seg_tokens);
 }
 
-// Called by one warp: index p among all segments (longest first), or among all
-// but each sequence's last, which are whole.
+// Called by one warp: index p among all segments (longest first), or among
+// those of the sequences that have several.
 __device__ __forceinline__ PlUnit find_segment(const int32_t* cu, int n_seqs, int tokens, int seg_tokens,
                                                bool all, int p) {
   const int kseg = length_class(seg_tokens / kPlTile);
   const PackedPiece w = find_piece(cu, n_seqs, tokens, all ? kseg : 0, p, [&](int n, int k) {
-    if (!all) return segments_of(n, seg_tokens) - 1;
+    const int n_seg = segments_of(n, seg_tokens);
+    if (!all) return n_seg > 1 ? n_seg : 0;
     const int whole = n / seg_tokens, rest = n - whole * seg_tokens;
     const bool has_rest = rest > 0 || n == 0;
     return (k == kseg ? whole : 0) + (has_rest && k == length_class((rest + kPlTile - 1) / kPlTile));
@@ -145,7 +150,7 @@ __device__ __forceinline__ PlUnit find_segment(const int32_t* cu, int n_seqs, in
     for (int i = threadIdx.x & 31; i < w.seq; i += 32)
       if (seq_ok(cu, i, tokens)) {
         const int e = segments_of(cu[i + 1] - cu[i], seg_tokens);
-        if (e > 1) before += e;
+        if (e > 1) before += e + 1;
       }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
@@ -198,15 +203,19 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t sr
                : "memory");
 }
 
-// bf16 pair (w) times (f, f): high and low bf16 parts.
-__device__ __forceinline__ void split_pair(uint32_t w, float f, uint32_t* hi, uint32_t* lo) {
+// bf16 pair (w) times (f, f) in three bf16 parts.
+__device__ __forceinline__ void split_pair(uint32_t w, float f, uint32_t* hi, uint32_t* lo, uint32_t* low) {
   const float2 x = __fmul2_rn(__bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w)), make_float2(f, f));
   const __nv_bfloat162 h = __floats2bfloat162_rn(x.x, x.y);
   const float2 hf = __bfloat1622float2(h);
   const float2 d = __fadd2_rn(x, make_float2(-hf.x, -hf.y));
   const __nv_bfloat162 l = __floats2bfloat162_rn(d.x, d.y);
+  const float2 lf = __bfloat1622float2(l);
+  const float2 e = __fadd2_rn(d, make_float2(-lf.x, -lf.y));
+  const __nv_bfloat162 m = __floats2bfloat162_rn(e.x, e.y);
   *hi = *reinterpret_cast<const uint32_t*>(&h);
   *lo = *reinterpret_cast<const uint32_t*>(&l);
+  *low = *reinterpret_cast<const uint32_t*>(&m);
 }
 
 // The warps that build P, split V and carry the state.  A function of its own,
@@ -214,7 +223,7 @@ __device__ __forceinline__ void split_pair(uint32_t w, float f, uint32_t* hi, ui
 // (inlined, the compiler keeps 30 of them in memory inside the loop over tiles).
 // What it needs rarely is in shared memory (PlShared), not among its arguments,
 // which the compiler would keep in memory too.
-template <int D, bool kOut>
+template <int D, bool kOut, bool kThree>
 __device__ __noinline__ void linear_state_role(uint32_t o_smem, uint32_t tmem, int n_tok, int nds, int flags) {
   using L = PlLayout;
   constexpr int NH = 128 / D;
@@ -412,7 +421,7 @@ __device__ __noinline__ void linear_state_role(uint32_t o_smem, uint32_t tmem, i
     if constexpr (kOut) {
       const bool want = c >= 0 && c < nds;
       if (c >= 0 && !(ok = __all_sync(0xffffffffu, tc::mbar_wait(bar + L::pv_done, c & 1)))) break;
-      uint4 lo[8] = {};
+      uint4 lo[8] = {}, low[8] = {};
       if (want) {
         const float f = r < Lt ? pwv[Lt - 1 - r] : 0.f;
         if (bad) {         // the state takes the row as it came
@@ -428,10 +437,10 @@ __device__ __noinline__ void linear_state_role(uint32_t o_smem, uint32_t tmem, i
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             uint4 hi;
-            split_pair(x[i].x, f, &hi.x, &lo[i0 + i].x);
-            split_pair(x[i].y, f, &hi.y, &lo[i0 + i].y);
-            split_pair(x[i].z, f, &hi.z, &lo[i0 + i].z);
-            split_pair(x[i].w, f, &hi.w, &lo[i0 + i].w);
+            split_pair(x[i].x, f, &hi.x, &lo[i0 + i].x, &low[i0 + i].x);
+            split_pair(x[i].y, f, &hi.y, &lo[i0 + i].y, &low[i0 + i].y);
+            split_pair(x[i].z, f, &hi.z, &lo[i0 + i].z, &low[i0 + i].z);
+            split_pair(x[i].w, f, &hi.w, &lo[i0 + i].w, &low[i0 + i].w);
             sts16(chunk(c, L::kV, i0 + i), hi);
           }
         }
@@ -448,11 +457,19 @@ __device__ __noinline__ void linear_state_role(uint32_t o_smem, uint32_t tmem, i
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(bar + L::v_lo);
       }
+      if (kThree && want) {
+        if (!(ok = __all_sync(0xffffffffu, tc::mbar_wait(bar + L::lo_done, c & 1)))) break;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sts16(chunk(c, L::kV, i), low[i]);
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(bar + L::v_low);
+      }
       if (c + 1 < nt) {
 #pragma unroll 1
         for (int hs = 0; ok && hs < NH; ++hs) ok = make_p(c + 1, hs);
-        if (!ok) break;
       }
+      if (!ok) break;
       if (want) {
         // the products being done says that Q S of this tile has read the copy of S too
         if (!(ok = join(c, bar + L::ds_full, c & 1, ds_addr))) break;
@@ -461,17 +478,22 @@ __device__ __noinline__ void linear_state_role(uint32_t o_smem, uint32_t tmem, i
       bad = bad_next;
     } else {
       const float f = r < Lt ? pwv[Lt - 1 - r] : 0.f;
+      uint4 low[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const uint4 x = lds16(chunk(c, L::kV, i));
         uint4 hi, lo;
-        split_pair(x.x, f, &hi.x, &lo.x);
-        split_pair(x.y, f, &hi.y, &lo.y);
-        split_pair(x.z, f, &hi.z, &lo.z);
-        split_pair(x.w, f, &hi.w, &lo.w);
+        split_pair(x.x, f, &hi.x, &lo.x, &low[i].x);
+        split_pair(x.y, f, &hi.y, &lo.y, &low[i].y);
+        split_pair(x.z, f, &hi.z, &lo.z, &low[i].z);
+        split_pair(x.w, f, &hi.w, &lo.w, &low[i].w);
         sts16(chunk(c, L::kV, i), hi);
         sts16(chunk(c, L::kQ, i), lo);
       }
+      // the third part's place is free once its products for the last tile are done
+      if (c > 0 && !(ok = __all_sync(0xffffffffu, tc::mbar_wait(bar + L::lo_done, (c - 1) & 1)))) break;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sts16(chunk(0, L::kS, i), low[i]);
       tc::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(bar + (c & 1 ? L::v_hi : L::kv_ok));
@@ -669,11 +691,10 @@ linear_packed_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
   const int s0 = cu[u.seq] + u.seg * seg_tokens;
   const int n_tok = min(cu[u.seq + 1] - s0, seg_tokens);
   const int nt = (n_tok + kPlTile - 1) / kPlTile;
-  const bool last = u.seg + 1 == u.n_seg;
   // the entering and the leaving state: rows of D values from `row` on, key dims
   // of the heads one after the other
   const bool has_src = kOut && (u.n_seg > 1 || (state_in && slot >= 0));
-  const bool has_dst = !kOut || (last && state_out && slot >= 0);
+  const bool has_dst = !kOut || (u.n_seg == 1 && state_out && slot >= 0);
   const int heads = min(NH, H - hg * NH);              // heads that exist
   const int own_row = (slot * H + hg * NH) * D;        // in the caller's pools
   if (nt == 0) {        // an empty sequence hands its state on
@@ -687,6 +708,9 @@ linear_packed_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
   }
   // tiles whose K^T V' is wanted
   const int nds = has_dst ? nt : nt - 1;
+  // A state that leaves keeps fp32's accuracy with V' in three parts; one that only
+  // Q multiplies, after a rounding to bf16, has two.
+  const bool three = has_dst;
   auto tile_len = [&](int c) { return min(kPlTile, n_tok - c * kPlTile); };
 
   if (threadIdx.x == 0) {
@@ -710,6 +734,8 @@ linear_packed_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
     tc::mbar_init(bars + L::v_hi / 8, 8);
     tc::mbar_init(bars + L::v_lo / 8, 8);
     tc::mbar_init(bars + L::hi_done / 8, 1);
+    tc::mbar_init(bars + L::v_low / 8, 8);
+    tc::mbar_init(bars + L::lo_done / 8, 1);
     tc::mbar_init(bars + L::fin / 8, 1);
     tc::mbar_init(bars + L::s_ld / 8, 1);
     tc::mbar_init(bars + L::e_sync / 8, 4);
@@ -795,7 +821,7 @@ linear_packed_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
           tc::mma_commit(bar + L::qk_full);
         };
         auto issue_ds = [&](int c, int which, uint32_t col, bool acc) {
-          const uint32_t k = part(c, L::kK), w = part(c, which);
+          const uint32_t k = part(c, L::kK), w = which == L::kS ? sb : part(c, which);
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
             tc::mma_bf16_ss(tmem + col, tc::smem_desc_sw128(k + kk * 2048, 16384, 1024),
@@ -858,19 +884,27 @@ linear_packed_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
               if (!(ok = tc::mbar_wait(bar + L::v_lo, c & 1))) break;
               tc::tc_fence_after();
               issue_ds(c, L::kV, L::kColDs, true);
+              if (three) {       // written once the second part has been read
+                tc::mma_commit(bar + L::lo_done);
+                if (!(ok = tc::mbar_wait(bar + L::v_low, c & 1))) break;
+                tc::tc_fence_after();
+                issue_ds(c, L::kV, L::kColDs, true);
+              }
               tc::mma_commit(bar + L::ds_full);
               tc::mma_commit(bar + L::ld_empty + 8 * (c & 1));
             }
           }
         } else {
-          // high parts lie in V's place, low parts in Q's
+          // the parts lie in V's place, in Q's, and in that of the copy of S
           for (int c = 0; ok && c < nt; ++c) {
             const int x = c & 1, use = c >> 1;
             if (!(ok = tc::mbar_wait(bar + L::ld_full + 8 * x, use & 1) && tc::mbar_wait(bar + (x ? L::v_hi : L::kv_ok), use & 1))) break;
             // (who wrote V' of this tile has read the sum of tile c - 2 before)
             tc::tc_fence_after();
-            issue_ds(c, L::kV, L::kColDs - 128 * (c & 1), false);
+            issue_ds(c, L::kS, L::kColDs - 128 * (c & 1), false);     // its place is free first
+            tc::mma_commit(bar + L::lo_done);
             issue_ds(c, L::kQ, L::kColDs - 128 * (c & 1), true);
+            issue_ds(c, L::kV, L::kColDs - 128 * (c & 1), true);
             tc::mma_commit(bar + L::ds_full + 8 * (c & 1));
             tc::mma_commit(bar + L::ld_empty + 8 * (c & 1));
           }
@@ -883,7 +917,9 @@ linear_packed_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
     if constexpr (kOut) linear_output_role<D>(tc::smem_u32(smem), tmem, n_tok);
     else tc::setmaxnreg_dec<kPlRegs2>();
   } else {
-    linear_state_role<D, kOut>(tc::smem_u32(smem), tmem, n_tok, nds, has_src | heads << 1);
+    const int flags = has_src | heads << 1;
+    if (!kOut || three) linear_state_role<D, kOut, true>(tc::smem_u32(smem), tmem, n_tok, nds, flags);
+    else linear_state_role<D, kOut, false>(tc::smem_u32(smem), tmem, n_tok, nds, flags);
   }
 
   tc::tc_fence_before();
@@ -895,15 +931,15 @@ linear_packed_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
 }
 
 // Between the two: the k-th sequence of several segments turns what each of
-// its segments but the last adds (entry s + 1 for segment s) into the state
-// that enters segment s (entry s).
+// its segments adds (entry s + 1 for segment s) into the state that enters
+// segment s (entry s), and hands on the last.
 // Four state values per thread.
 constexpr int kPlScanThreads = 256;
 
 template <int D>
 __global__ void __launch_bounds__(kPlScanThreads)
 linear_packed_scan_kernel(const float* __restrict__ lambda, const int32_t* __restrict__ cu,
-                          const int32_t* __restrict__ slots, const float* __restrict__ state_in, float* ws,
+                          const int32_t* __restrict__ slots, const float* state_in, float* state_out, float* ws,
                           int tokens, int n_seqs, int n_slots, int H, int seg_tokens) {
   __shared__ PlUnit unit;
   if (threadIdx.x < 32) {
@@ -915,12 +951,12 @@ linear_packed_scan_kernel(const float* __restrict__ lambda, const int32_t* __res
       const int i = i0 + lane;
       int e = 0;
       if (i < n_seqs && seq_ok(cu, i, tokens)) e = (cu[i + 1] - cu[i] + seg_tokens - 1) / seg_tokens;
-      if (e < 2) e = 0;
+      e = e < 2 ? 0 : e + 1;
       const unsigned multi = __ballot_sync(0xffffffffu, e > 0);
       if (k < __popc(multi)) {
         const int w = __fns(multi, 0, k + 1);
         u.seq = i0 + w;
-        u.n_seg = __shfl_sync(0xffffffffu, e, w);
+        u.n_seg = __shfl_sync(0xffffffffu, e, w) - 1;
         int before = lane < w ? e : 0;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
@@ -941,13 +977,15 @@ linear_packed_scan_kernel(const float* __restrict__ lambda, const int32_t* __res
   const long long e = 4 * ((long long)blockIdx.x * kPlScanThreads + threadIdx.x);
   const long long per = (long long)H * D * D;
   if (e >= per) return;
-  const float f = decay_pow(lambda[e / (D * D)], seg_tokens);
+  const float lam = lambda[e / (D * D)];
+  const float whole = decay_pow(lam, seg_tokens);
+  const int n = u.n_seg;
+  const float rest = decay_pow(lam, cu[u.seq + 1] - cu[u.seq] - (n - 1) * seg_tokens);
   float4 S = make_float4(0.f, 0.f, 0.f, 0.f);
   if (state_in && slot >= 0) S = *reinterpret_cast<const float4*>(state_in + slot * per + e);
   float* p = ws + u.ws * per + e;
   *reinterpret_cast<float4*>(p) = S;           // state_out may be state_in: the outputs read it from here
   p += per;
-  const int n = u.n_seg - 1;
   for (int s0 = 0; s0 < n; s0 += 8) {          // eight sums in flight
     float4 x[8];
 #pragma unroll
@@ -956,13 +994,16 @@ linear_packed_scan_kernel(const float* __restrict__ lambda, const int32_t* __res
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       if (s0 + i < n) {
+        const bool end = s0 + i + 1 == n;
+        const float f = end ? rest : whole;
         S.x = fmaf(f, S.x, x[i].x);
         S.y = fmaf(f, S.y, x[i].y);
         S.z = fmaf(f, S.z, x[i].z);
         S.w = fmaf(f, S.w, x[i].w);
-        *reinterpret_cast<float4*>(p + (s0 + i) * per) = S;
+        if (!end) *reinterpret_cast<float4*>(p + (s0 + i) * per) = S;
       }
   }
+  if (state_out && slot >= 0) *reinterpret_cast<float4*>(state_out + slot * per + e) = S;
 }
 
 }  // namespace sala

@@ -13,8 +13,11 @@ step: bf16 2^-8, relative):
     (2^-8 |q k|) to bf16: at most 2^-8 |q| Sabs with Sabs the recurrence of the
     absolute values.  Norm-wise these three independent roundings (each at most
     2^-8, root mean square below 2^-9 2/sqrt(3)) stay below 2^-8;
-  * states take decayed keys or values split into two bf16 parts: 2^-16 Sabs,
-    and fp32 sums of n terms: below 2^-17 Sabs for the lengths used here.
+  * states take decayed values split into three bf16 parts (2^-24), and fp32 sums
+    of up to 3 x 128 terms per tile on the tensor core, which may round towards
+    zero (2^-23 each): 2^-23 x 384 Sabs is below 2^-14, in practice far below:
+    terms of both signs cancel in their roundings.  Element-wise 2^-16 Sabs is
+    asked for, norm-wise 2^-20.
 """
 import ctypes
 import math
@@ -472,7 +475,7 @@ def test_dense_is_deterministic_on_streams_and_in_graphs(cuda_device):
 # ---------------------------------------------------------------------------------------- linear
 
 LINEAR = [([1], 1, 64), ([3, 0, 1], 4, 64), ([128], 2, 128), ([127, 129, 64], 3, 128), ([1000, 5], 2, 128),
-          ([70, 333], 8, 64), ([2600], 1, 128)]
+          ([70, 333], 8, 64), ([2600], 1, 128), ([2100, 40, 1500], 3, 64)]
 
 
 def lin_check(out, ref, mag):
@@ -506,8 +509,8 @@ def test_linear_packed_prefill(cuda_device, lens, H, d, with_state):
     assert bool((out[:before] == 7).all()) and bool((out[cu[-1]:] == 7).all())
     if with_state:
         for p, S, A in zip(slots.tolist(), fin, fabs):
-            check(fin_pool[p], S, (2.0 ** -16 + 2.0 ** -17) * A + 1e-30)
-            assert float((fin_pool[p].double() - S).norm() / S.norm()) < 1e-5
+            check(fin_pool[p], S, 2.0 ** -16 * A + 1e-30)
+            assert float((fin_pool[p].double() - S).norm() / S.norm()) < 2.0 ** -20
         others = [i for i in range(n + 2) if i not in slots.tolist()]
         assert bool((fin_pool[others] == 3).all())
         sala.linear_packed_prefill(q, k, v, gate, lam, i32(cu), slots=slots, state_in=pool, state_out=pool,
@@ -530,7 +533,7 @@ def test_linear_packed_special_decays(cuda_device, value, d):
     ref, mag, S, A = ref_linear(q, k, v, gate, lam, cu, [pool[0], pool[1]])
     lin_check(out, ref, mag)
     for i in range(2):
-        check(fin[i], S[i], (2.0 ** -16 + 2.0 ** -17) * A[i] + 1e-30)
+        check(fin[i], S[i], 2.0 ** -16 * A[i] + 1e-30)
 
 
 @pytest.mark.gpu
@@ -548,7 +551,7 @@ def test_linear_packed_slots(cuda_device):
         ref, mag, S, A = ref_linear(q, k, v, gate, lam, cu, [pool[1], None, pool[0], None])
         lin_check(out, ref, mag)
         for i, p in ((0, 1), (2, 0)):
-            check(fin[p], S[i], (2.0 ** -16 + 2.0 ** -17) * A[i] + 1e-30)
+            check(fin[p], S[i], 2.0 ** -16 * A[i] + 1e-30)
 
 
 @pytest.mark.gpu
@@ -589,7 +592,7 @@ def test_linear_packed_bad_bounds(cuda_device):
     assert bool((out[4:] == 7).all()) and bool((fin[1:] == 3).all())
     ref, mag, S, A = ref_linear(q, k, v, gate, decays(2), [0, 4], [pool[0]])
     lin_check(out[:4], ref[:4], mag[:4])
-    check(fin[0], S[0], (2.0 ** -16 + 2.0 ** -17) * A[0] + 1e-30)
+    check(fin[0], S[0], 2.0 ** -16 * A[0] + 1e-30)
 
 
 @pytest.mark.gpu
@@ -854,4 +857,4 @@ def test_serving_run(cuda_device, d, H, Hq, Hkv):
         have += 1
     clean()
     for i, s in enumerate([2, 0, 1]):
-        check(pool[s], fin[i], (2.0 ** -16 + 2.0 ** -17) * fabs[i] + 1e-30)
+        check(pool[s], fin[i], 2.0 ** -16 * fabs[i] + 1e-30)
