@@ -19,9 +19,8 @@
 // PV(1), ...: tcgen05.mma of one thread execute in order, so S(i+1) may
 // overwrite P(i), and S(i+1) being complete says that PV(i) is too.  The
 // running maximum is raised (O and l rescaled) only when a row's maximum grew
-// by more than 2^8; l is the fp32 sum of the weights before their rounding to
-// bf16 (half a step, 2^-9 of each weight on average below that: the output is
-// rounded to bf16 itself).
+// by more than 2^8.  P is rounded to bf16 for its product, which is of the size
+// of the output's own rounding; l sums the weights before that, in fp32.
 //
 // Isolation: a masked key has weight 0, but 0 x NaN and 0 x infinity are NaN
 // on the tensor core.  In the blocks that hold masked keys (those on the
@@ -30,7 +29,15 @@
 // adds to the rows that do see them.
 //
 // Bound by the tensor core and, with it, the exponentials (128 x 128 of them
-// per tile and block take as long as its two products).
+// per tile and block take as long as its two products).  One prompt of 32768
+// tokens, 32 q heads over 2 kv heads, d = 128: 7.6 ms, 1160 TFLOP/s, 72 % of what
+// this card's library product of 8192^3 reaches in a burst and 84 % of what it
+// sustains.  Measured around it: P in one piece instead of two halves 7.8 ms;
+// 1, 3 and 4 of 8 pairs of exponentials on the FMA pipe 7.67, 7.56 and 7.89 ms
+// (none: 7.63); logits read from TMEM 32 at a time in rolled loops, without the 128
+// registers, 8.2 to 8.4 ms.  Short prompts cost the set-up: 333 tokens in 6
+// prompts take 9 us in one wave, 1.8 us until the first key block has landed and
+// 1.3 us per block.
 #pragma once
 
 #include "common.cuh"
@@ -43,7 +50,6 @@ constexpr int kPaBlock = 128;                // keys per block
 constexpr int kPaRegsLow = 72, kPaRegsHigh = 216;
 constexpr float kPaRescale = 8.0f;           // log2 units
 constexpr float kPaLowest = -3.402823466e38f;
-constexpr int kPaPolyPairsPer8 = 0;          // exponential pairs evaluated on the FMA pipe
 
 template <int D>
 struct PaLayout {
@@ -414,9 +420,7 @@ __device__ __forceinline__ void pa_run(const CUtensorMap& qmap, const CUtensorMa
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           const float2 z = __ffma2_rn(make_float2(x[32 * q0 + 2 * e], x[32 * q0 + 2 * e + 1]), sl2v, negm);
-          const float2 pv = (e & 7) < kPaPolyPairsPer8
-                                ? tc::exp2_fma2(z)
-                                : make_float2(tc::ex2_approx(z.x), tc::ex2_approx(z.y));
+          const float2 pv = make_float2(tc::ex2_approx(z.x), tc::ex2_approx(z.y));
           acc4[e & 3] = __fadd2_rn(acc4[e & 3], pv);
           __nv_bfloat162 h2 = __floats2bfloat162_rn(pv.x, pv.y);
           pk[e] = *reinterpret_cast<uint32_t*>(&h2);

@@ -14,6 +14,10 @@
 // halves (a rotation pair each), so a warp reads whole rows, four at a time for
 // each thread; the cosines and sines of a token are formed once in shared
 // memory and serve all its heads.
+//
+// 32768 tokens, 32 + 32 heads of 128, RoPE: 209 us, 5.1 TB/s (78 % of the copy
+// rate).  Rows of a thread in flight: 1 281 us, 2 253, 4 209, 8 531 (spills);
+// CTAs of 256 threads 227 us, of 64 207; 8 or 16 tokens per CTA the same.
 #pragma once
 
 #include "common.cuh"

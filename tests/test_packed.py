@@ -581,6 +581,21 @@ def test_linear_packed_isolation(cuda_device, bad):
 
 
 @pytest.mark.gpu
+def test_linear_packed_heads_side_by_side(cuda_device):
+    """Two heads of 64 share a tile: NaN in one leaves the other's bits as they are."""
+    cu = [0, 150, 200]
+    q, k, v, gate = linear_inputs(200, 3, 64, seed=3)
+    lam, a, b = decays(3), torch.empty((2, 3, 64, 64), device="cuda"), torch.empty((2, 3, 64, 64), device="cuda")
+    want = sala.linear_packed_prefill(q, k, v, gate, lam, i32(cu), state_out=a)
+    q[5, 1], k[140, 1], v[160, 1] = math.nan, math.inf, math.nan
+    got = sala.linear_packed_prefill(q, k, v, gate, lam, i32(cu), state_out=b)
+    clean()
+    assert torch.equal(got[:, ::2], want[:, ::2]) and torch.equal(a[:, ::2], b[:, ::2])
+    assert bool(got[5, 1].isnan().all()) and torch.equal(got[6:140, 1], want[6:140, 1])
+    assert not bool(got[140:150, 1].isfinite().any()) and torch.equal(got[150:160, 1], want[150:160, 1])
+
+
+@pytest.mark.gpu
 def test_linear_packed_bad_bounds(cuda_device):
     q, k, v, gate = linear_inputs(10, 2, 64)
     pool = torch.ones((3, 2, 64, 64), device="cuda")
