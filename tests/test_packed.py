@@ -644,6 +644,37 @@ def test_linear_packed_graphs_with_a_workspace_each(cuda_device):
     assert torch.equal(runs[0][2], want) and torch.equal(runs[0][3], fin)
 
 
+MANY = [(37 * i * i) % 211 for i in range(70)] + [2500, 1, 0]
+
+
+@pytest.mark.gpu
+def test_many_sequences(cuda_device):
+    """More sequences than a warp looks at together, a long one that is cut behind them."""
+    cu = starts(MANY)
+    T, n = cu[-1], len(MANY)
+    q, k, v, gate = dense_inputs(T, 4, 2, 128, seed=4)
+    out = sala.dense_prefill(q, k, v, gate, i32(cu))
+    ref, mag = ref_dense(q, k, v, gate, cu)
+    check(out, ref, attn_tol(ref, mag))
+    q, k, v, gate = linear_inputs(T, 2, 128, seed=4)
+    lam = decays(2)
+    pool = torch.randn((n, 2, 128, 128), generator=gen(4), device="cuda")
+    fin = torch.empty_like(pool)
+    ref, mag, S, A = ref_linear(q, k, v, gate, lam, cu, list(pool))
+    out = sala.linear_packed_prefill(q, k, v, gate, lam, i32(cu), state_in=pool, state_out=fin)
+    lin_check(out, ref, mag)
+    for i in range(n):
+        check(fin[i], S[i], 2.0 ** -16 * A[i] + 1e-30)
+    out = sala.linear_packed_prefill(q, k, v, gate, lam, i32(cu), state_in=pool)      # outputs only
+    lin_check(out, ref, mag)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    again = sala.linear_packed_prefill(q, k, v, gate, lam, i32(cu), state_in=pool, stream=s)
+    s.synchronize()
+    assert torch.equal(out, again)
+    clean()
+
+
 # ------------------------------------------------------------------------------------------ step
 
 @pytest.mark.gpu
@@ -795,6 +826,19 @@ def test_prefix_decode_graph_follows_lengths(cuda_device):
         ref, mag = ref_prefix(t["q"], t["k"], t["v"], t["gate"], t["pk"], t["pv"], t["kc"], t["vc"], new, t["slots"])
         check(out, ref, attn_tol(ref, mag))
         assert torch.equal(call(None), out)          # the same call gives the same bits
+
+
+@pytest.mark.gpu
+def test_prefix_decode_without_slots_and_on_a_stream(cuda_device):
+    t = prefix_inputs(5, 300, 100, 8, 2, 64, 7, seed=2)
+    t["slots"] = list(range(5))
+    ref, mag = ref_prefix(t["q"], t["k"], t["v"], t["gate"], t["pk"], t["pv"], t["kc"], t["vc"], t["lens"], t["slots"])
+    lens, s = i32(t["lens"]), torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    out = sala.prefix_decode(t["q"], t["k"], t["v"], t["gate"], t["pk"], t["pv"], t["kc"], t["vc"], lens, stream=s)
+    s.synchronize()
+    check(out, ref, attn_tol(ref, mag))
+    clean()
 
 
 @pytest.mark.gpu
