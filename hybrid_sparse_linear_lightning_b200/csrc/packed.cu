@@ -237,7 +237,9 @@ sala_status run_linear(const sala_packed_linear_desc* d, const void* q, const vo
 // How a decode step over a shared prefix is cut up.
 struct PrefixPlan {
   int Tt, pairs;                 // requests per row tile, pairs of row tiles
-  int split_blocks, n_split;     // key blocks per part of the prefix, parts
+  int mtiles;                    // 16-row tiles of a group
+  bool walked;                   // the prefix is read with each request's own keys
+  int split_blocks, n_split;     // else: key blocks per part of the prefix, parts
   size_t o, ml, total;           // workspace: parts of O, of (maximum, sum)
 };
 
@@ -248,7 +250,9 @@ PrefixPlan prefix_plan(const sala_prefix_desc* d) {
   const int64_t tiles = ((int64_t)d->batch + p.Tt - 1) / p.Tt;
   p.pairs = (int)((tiles + 1) / 2);
   const int64_t blocks = ((int64_t)d->prefix_len + kPaBlock - 1) / kPaBlock;
-  if (blocks > 0) {
+  p.mtiles = (d->q_heads / d->kv_heads + 15) / 16;
+  p.walked = (double)d->batch * d->kv_heads * p.mtiles * d->prefix_len * d->head_dim * 4 <= 24e6;
+  if (blocks > 0 && !p.walked) {
     // the number of parts whose waves of units take the fewest block times; a
     // unit costs two blocks' time to start and to hand over its part
     const int64_t units = d->kv_heads * (int64_t)p.pairs;
@@ -299,10 +303,13 @@ sala_status run_prefix(const sala_prefix_desc* d, const void* q, const void* k, 
   }
   // clusters grow until their CTAs fill the card twice over (two CTAs live on an
   // SM), as long as every warp has eight steps of a full cache
-  const int mtiles = (G + 15) / 16;
+  const int mtiles = p.mtiles, walked = p.walked ? d->prefix_len : 0;
   const int64_t units = (int64_t)d->batch * d->kv_heads * mtiles;
+  const int64_t keys = d->cache_capacity + walked;
   int cs = 1;
-  while (cs < kOwnMaxCluster && units * cs < 4 * 148 && d->cache_capacity > (int64_t)cs * kOwnWarps * 16 * 8) cs *= 2;
+  while (cs < kOwnMaxCluster && units * cs < 4 * 148 && keys > (int64_t)cs * kOwnWarps * 16 * 8) cs *= 2;
+  // and over SMs that would stay idle down to two steps
+  while (cs < kOwnMaxCluster && units * cs * 2 <= 148 && keys > (int64_t)cs * kOwnWarps * 16 * 2) cs *= 2;
   if (units * cs > 0x7fffffffll) return SALA_ERR_UNSUPPORTED;
   auto kern = own_attn_kernel<D>;
   const size_t smem = OwnLayout<D>::kBytes;
@@ -322,10 +329,10 @@ sala_status run_prefix(const sala_prefix_desc* d, const void* q, const void* k, 
   cfg.attrs = attr;
   cfg.numAttrs = p.n_split > 0 ? 2 : 1;    // alone, the kernel starts after what came before it
   cudaLaunchKernelEx(&cfg, kern, static_cast<const bf16*>(q), static_cast<const bf16*>(k),
-                     static_cast<const bf16*>(v), static_cast<const bf16*>(gate), static_cast<bf16*>(kc),
-                     static_cast<bf16*>(vc), lens, slots, static_cast<const float*>(part_o),
+                     static_cast<const bf16*>(v), static_cast<const bf16*>(gate), static_cast<const bf16*>(pk),
+                     static_cast<const bf16*>(pv), static_cast<bf16*>(kc), static_cast<bf16*>(vc), lens, slots, static_cast<const float*>(part_o),
                      static_cast<const float2*>(part_ml), static_cast<bf16*>(out), d->batch, d->q_heads,
-                     d->kv_heads, mtiles, p.n_split, (long long)d->cache_capacity, d->n_slots, sl2);
+                     d->kv_heads, mtiles, walked, p.n_split, (long long)d->cache_capacity, d->n_slots, sl2);
   return launch_status();
 }
 

@@ -395,8 +395,8 @@ sala_status sala_linear_packed_step(const sala_packed_linear_desc* d, const void
 
 /* One decode token of each of `batch` requests that share their first
  * prefix_len tokens, through the sparse layer's dense form: the prefix's keys
- * and values are read once for the whole batch.  SALA_BF16; q_heads /
- * kv_heads up to 128. */
+ * and values are read once for the whole batch (or, where they are few, with
+ * each request's own).  SALA_BF16; q_heads / kv_heads up to 128. */
 typedef struct {
   int batch, prefix_len;     /* prefix_len >= 0                                */
   int n_slots, q_heads, kv_heads, head_dim;

@@ -727,7 +727,7 @@ def test_linear_packed_step_doubled_slots(cuda_device):
 
 PREFIX = [(1, 0, 1, 1, 1, 64), (5, 70, 48, 4, 1, 64), (3, 128, 300, 6, 2, 128), (9, 1000, 700, 16, 1, 128),
           (130, 257, 20, 3, 3, 64), (2, 2000, 64, 128, 1, 128), (4, 0, 513, 32, 8, 128), (3, 1, 1300, 7, 1, 64),
-          (6, 640, 130, 100, 1, 64)]
+          (6, 640, 130, 100, 1, 64), (40, 1500, 64, 8, 2, 128), (20, 5000, 33, 7, 1, 64), (33, 1025, 200, 24, 3, 128)]
 
 
 def prefix_inputs(B, P, cap, Hq, Hkv, d, n_slots, seed=0):
@@ -808,8 +808,9 @@ def test_prefix_decode_isolation(cuda_device):
 
 
 @pytest.mark.gpu
-def test_prefix_decode_graph_follows_lengths(cuda_device):
-    t = prefix_inputs(5, 500, 300, 8, 1, 128, 5, seed=8)
+@pytest.mark.parametrize("P", [500, 12000])
+def test_prefix_decode_graph_follows_lengths(cuda_device, P):
+    t = prefix_inputs(5, P, 300, 8, 1, 128, 5, seed=8)
     lens, slots = i32([10, 0, 299, 130, 1]), i32(t["slots"])
     out = torch.empty_like(t["q"])
     g = torch.cuda.CUDAGraph()
