@@ -227,7 +227,8 @@ sala_status run_linear(const sala_packed_linear_desc* d, const void* q, const vo
                     (unsigned)p.multi);
     if (grid.y > 65535) return SALA_ERR_UNSUPPORTED;
     linear_packed_scan_kernel<D><<<grid, kPlScanThreads, 0, st>>>(
-        lambda, cu, slots, state_in, state_out, ws, d->tokens, d->n_seqs, d->n_slots, d->heads, p.seg_tokens);
+        lambda, cu, slots, state_in, state_out, ws, d->tokens, d->n_seqs, d->n_slots, d->heads, p.seg_tokens,
+        (int)p.entries);
     s = launch_status();
     if (s != SALA_OK) return s;
   }

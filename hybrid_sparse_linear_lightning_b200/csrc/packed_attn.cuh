@@ -520,10 +520,42 @@ __device__ __forceinline__ void pa_run(const CUtensorMap& qmap, const CUtensorMa
   }
 }
 
-// Bounds of sequence i are usable.
+// Bounds of sequence i are usable by themselves.
 __device__ __forceinline__ bool seq_ok(const int32_t* cu, int i, int tokens) {
   return cu[i] >= 0 && cu[i] <= cu[i + 1] && cu[i + 1] <= tokens;
 }
+
+// Lengths of sequences i0 .. i0 + 31, one per lane of a warp that asks for i0 = 0,
+// 32, ... in turn; -1 where there is none or it is skipped.  Skipped is a sequence
+// whose bounds are not usable, and one that begins below the end of an earlier
+// usable one: those that are left are disjoint, and the grids and workspaces, sized
+// from the number of tokens, hold their pieces.  Bounds that ascend need no more
+// than a vote.  Overlap takes a descent somewhere, so the look at each pair of
+// bounds, which sets the status, finds every call that holds a skipped sequence.
+struct SeqLengths {
+  int top = 0;       // highest end so far
+  __device__ __forceinline__ int next(const int32_t* cu, int n_seqs, int tokens, int i0) {
+    const int lane = threadIdx.x & 31, i = i0 + lane;
+    const bool in = i < n_seqs;
+    const int a = in ? cu[i] : 0, b = in ? cu[i + 1] : 0;
+    bool ok = in && a >= 0 && a <= b && b <= tokens;
+    int end = ok ? b : 0;
+    if (__all_sync(0xffffffffu, !in || (ok && a >= top))) {
+      end = __shfl_sync(0xffffffffu, end, min(31, n_seqs - 1 - i0));
+    } else {
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, end, o);
+        if (lane >= o) end = max(end, v);
+      }
+      const int before = __shfl_up_sync(0xffffffffu, end, 1);
+      ok = ok && a >= (lane > 0 ? max(top, before) : top);
+      end = __shfl_sync(0xffffffffu, end, 31);
+    }
+    top = max(top, end);
+    return ok ? b - a : -1;
+  }
+};
 
 // Work of different lengths, longest first: a launch's last blocks are then
 // short ones, which keeps all SMs busy to its end.  Lengths are compared by
@@ -539,13 +571,13 @@ template <typename Count>
 __device__ __forceinline__ PackedPiece find_piece(const int32_t* cu, int n_seqs, int tokens, int kmax, int p,
                                                   Count count) {
   const int lane = threadIdx.x & 31;
-  auto length = [&](int i) { return i < n_seqs && seq_ok(cu, i, tokens) ? cu[i + 1] - cu[i] : -1; };
-  int len = length(lane);
+  int len = SeqLengths().next(cu, n_seqs, tokens, 0);
 #pragma unroll 1
-  for (int k = kmax; k >= 0; --k)
+  for (int k = kmax; k >= 0; --k) {
+    SeqLengths walk;
 #pragma unroll 1
     for (int i0 = 0; i0 < n_seqs; i0 += 32) {
-      if (n_seqs > 32) len = length(i0 + lane);
+      if (n_seqs > 32) len = walk.next(cu, n_seqs, tokens, i0);
       const int n = len >= 0 ? count(len, k) : 0;
       int inc = n;
 #pragma unroll
@@ -560,6 +592,7 @@ __device__ __forceinline__ PackedPiece find_piece(const int32_t* cu, int n_seqs,
       }
       p -= __shfl_sync(0xffffffffu, inc, 31);
     }
+  }
   return PackedPiece{-1, 0, 0};
 }
 

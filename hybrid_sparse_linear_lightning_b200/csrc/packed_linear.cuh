@@ -154,11 +154,12 @@ __device__ __forceinline__ PlUnit find_segment(const int32_t* cu, int n_seqs, in
   u.seg = !all || w.cls == kseg ? w.idx : u.n_seg - 1;
   if (u.n_seg > 1) {
     int before = 0;
-    for (int i = threadIdx.x & 31; i < w.seq; i += 32)
-      if (seq_ok(cu, i, tokens)) {
-        const int e = segments_of(cu[i + 1] - cu[i], seg_tokens);
-        if (e > 1) before += e + 1;
-      }
+    SeqLengths walk;
+    for (int i0 = 0; i0 < w.seq; i0 += 32) {
+      const int len = walk.next(cu, n_seqs, tokens, i0);
+      const int e = segments_of(len, seg_tokens);
+      if (e > 1 && i0 + (int)(threadIdx.x & 31) < w.seq) before += e + 1;
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
     u.ws = before;
@@ -947,17 +948,16 @@ template <int D>
 __global__ void __launch_bounds__(kPlScanThreads)
 linear_packed_scan_kernel(const float* __restrict__ lambda, const int32_t* __restrict__ cu,
                           const int32_t* __restrict__ slots, const float* state_in, float* state_out, float* ws,
-                          int tokens, int n_seqs, int n_slots, int H, int seg_tokens) {
+                          int tokens, int n_seqs, int n_slots, int H, int seg_tokens, int entries) {
   __shared__ PlUnit unit;
   if (threadIdx.x < 32) {
     // the k-th sequence that has more than one segment
     int k = blockIdx.y, base = 0;
     PlUnit u = {-1, 0, 0, 0};
     const int lane = threadIdx.x;
+    SeqLengths walk;
     for (int i0 = 0; i0 < n_seqs; i0 += 32) {
-      const int i = i0 + lane;
-      int e = 0;
-      if (i < n_seqs && seq_ok(cu, i, tokens)) e = (cu[i + 1] - cu[i] + seg_tokens - 1) / seg_tokens;
+      int e = segments_of(walk.next(cu, n_seqs, tokens, i0), seg_tokens);
       e = e < 2 ? 0 : e + 1;
       const unsigned multi = __ballot_sync(0xffffffffu, e > 0);
       if (k < __popc(multi)) {
@@ -980,6 +980,12 @@ linear_packed_scan_kernel(const float* __restrict__ lambda, const int32_t* __res
   __syncthreads();
   const PlUnit u = unit;
   if (u.seq < 0) return;
+  // the plan has room for all sequences that are not skipped; bounds that another
+  // stream changes while the call runs may still ask for more
+  if (u.ws + u.n_seg + 1 > entries) {
+    if (threadIdx.x == 0) set_status(kStatusBounds);
+    return;
+  }
   const int slot = take_slot(slots, u.seq, n_slots);
   const long long e = 4 * ((long long)blockIdx.x * kPlScanThreads + threadIdx.x);
   const long long per = (long long)H * D * D;

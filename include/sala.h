@@ -312,7 +312,9 @@ sala_status sala_decode_step(const sala_decode_desc* d, const sala_decode_io* io
  *     Lengths need be multiples of nothing; 0 and 1 are lengths.  Rows before
  *     the first sequence and behind the last one are neither read for another
  *     row's result nor written.  A sequence whose bounds descend or leave
- *     [0, tokens] is skipped and sets the bounds bit of the status word.
+ *     [0, tokens] is skipped and sets the bounds bit of the status word; so is
+ *     one that begins below the end of an earlier sequence with usable bounds
+ *     (rows belong to one sequence at most).
  *   - Sequences are isolated: whatever one holds (NaN and infinities too), the
  *     others' results do not change; nor do those of a sequence's own earlier
  *     tokens.

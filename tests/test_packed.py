@@ -918,3 +918,79 @@ def test_serving_run(cuda_device, d, H, Hq, Hkv):
     clean()
     for i, s in enumerate([2, 0, 1]):
         check(pool[s], fin[i], 2.0 ** -16 * fabs[i] + 1e-30)
+
+
+# ------------------------------------------------------------------------- bounds that go back
+
+def usable(cu, T):
+    """Sequences that a call computes: usable bounds, and no start below the end of an earlier usable one."""
+    top, good = 0, []
+    for i, (a, b) in enumerate(zip(cu[:-1], cu[1:])):
+        if 0 <= a <= b <= T:
+            if a >= top:
+                good.append(i)
+            top = max(top, b)
+    return good
+
+
+# 2500 tokens: two heads of 128 are cut into segments of 1024, three for a whole sequence
+BACK = [[0, 2500, 0, 2500], [0, 2500, 0, 2500, 0, 2500], [0, 1100, 500, 2500], [2000, 1000, 1000, 2500],
+        [0, 9999, 40, 2500], [7, 7, 3, 1200, 1200], list(range(0, 1201, 30)) + [600, 1500, 2500, 100, 200]]
+
+
+def test_usable_sequences_are_disjoint():
+    for cu in BACK:
+        good = usable(cu, 2500)
+        assert 1 <= len(good) < len(cu) - 1
+        assert all(cu[i + 1] <= cu[j] for i, j in zip(good[:-1], good[1:]))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("cu", BACK)
+def test_linear_packed_bounds_that_go_back(cuda_device, cu):
+    """Sequences that overlap an earlier one are skipped, and the workspace is kept to."""
+    T, H, d, n = 2500, 2, 128, len(cu) - 1
+    q, k, v, gate = linear_inputs(T, H, d, seed=7)
+    lam = decays(H)
+    pool = torch.randn((n, H, d, d), generator=gen(4), device="cuda")
+    fin = torch.full_like(pool, 3.0)
+    out = torch.full((T, H, d), 7.0, dtype=BF, device="cuda")
+    desc = sala.PackedLinearDesc(T, n, n, H, d, sala.SALA_BF16, 1.0)
+    need = sala.LIB.sala_linear_packed_workspace_size(ctypes.byref(desc))
+    assert need > 0
+    guard = 64 * H * d * d * 4
+    ws = torch.full((need + guard,), 0x5a, dtype=torch.uint8, device="cuda")
+    sala.linear_packed_prefill(q, k, v, gate, lam, i32(cu), state_in=pool, state_out=fin, out=out, ws=ws)
+    torch.cuda.synchronize()
+    assert sala.sala_get_device_status() == sala.SALA_ERR_DEVICE_FAULT
+    assert sala.sala_get_device_status() == sala.SALA_OK
+    assert bool((ws[need:] == 0x5a).all())
+    untouched = torch.ones(T, dtype=torch.bool, device="cuda")
+    for i in usable(cu, T):
+        a, b = cu[i], cu[i + 1]
+        untouched[a:b] = False
+        ref, mag, S, A = ref_linear(q, k, v, gate, lam, [a, b], [pool[i]])
+        if b > a:
+            lin_check(out[a:b], ref[a:b], mag[a:b])
+        check(fin[i], S[0], 2.0 ** -16 * A[0] + 1e-30)
+    assert bool((out[untouched] == 7).all())
+    skipped = [i for i in range(n) if i not in usable(cu, T)]
+    assert bool((fin[skipped] == 3).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("cu", BACK)
+def test_dense_bounds_that_go_back(cuda_device, cu):
+    T, d = 2500, 64
+    q, k, v, gate = dense_inputs(T, 2, 1, d, seed=7)
+    out = torch.full((T, 2, d), 7.0, dtype=BF, device="cuda")
+    sala.dense_prefill(q, k, v, gate, i32(cu), out=out)
+    torch.cuda.synchronize()
+    assert sala.sala_get_device_status() == sala.SALA_ERR_DEVICE_FAULT
+    untouched = torch.ones(T, dtype=torch.bool, device="cuda")
+    for i in usable(cu, T):
+        a, b = cu[i], cu[i + 1]
+        untouched[a:b] = False
+        ref, mag = ref_dense(q, k, v, gate, [a, b])
+        check(out[a:b], ref[a:b], attn_tol(ref, mag)[a:b])
+    assert bool((out[untouched] == 7).all())
