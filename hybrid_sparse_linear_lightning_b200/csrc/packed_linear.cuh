@@ -24,6 +24,13 @@
 // and the copy of S that Q multiplies are rounded to bf16; Q, K and V enter as
 // they are.
 //
+// The gate's sigmoid is an exponential and a reciprocal, as in the other calls: a
+// closed gate's output keeps its relative accuracy.  1/2 + tanh(g / 2) / 2 on the
+// hardware's tanh takes half the special-function operations (64K prompt 912 us),
+// but its error of 2^-12 is absolute: 10 % of the output at g = -6.  Every other
+// exponential on the FMA pipe, or one reciprocal for two values, gain nothing (980
+// and 1075 us).
+//
 // Isolation.  Rows past a sequence's end become 0 in K and V before anything is
 // multiplied (0 x NaN is NaN).  So do non-finite values of V before P V, whose
 // zeros above the diagonal would else hand them to earlier tokens; the epilogue
@@ -34,7 +41,7 @@
 // is the chain of a tile through the warps that build P, split V and carry S, and
 // shared memory, which the products, the tiles and the staged outputs share (670
 // KB per tile, 5250 cycles): 9000 cycles per tile.  One prompt of 65536 tokens, 32
-// heads: 1.01 ms, 2.65 TB/s; 13 prompts of 9001 tokens: 191 us.  What it took: the
+// heads: 980 us, 2.74 TB/s; 13 prompts of 9001 tokens: 190 us.  What it took: the
 // roles as functions of their own (their registers in memory cost 3000 cycles per
 // tile), loops rolled to fit the instruction caches, V and S shared by two
 // warpgroups, outputs in 128-byte pieces, states by TMA (12 us less per CTA than
@@ -165,28 +172,6 @@ __device__ __forceinline__ PlUnit find_segment(const int32_t* cu, int n_seqs, in
     u.ws = before;
   }
   return u;
-}
-
-// sigmoid(g) o for eight values, with the sigmoid of the linear layers:
-// 1/2 + tanh(g / 2) / 2 on the hardware's tanh (absolute error 2^-12), half the
-// special-function operations of an exponential and a reciprocal, which take
-// 4000 cycles of the 8000 that a tile's outputs have.
-__device__ __forceinline__ uint4 gate_pack_tanh(const uint4& g, const uint4& a, const uint4& b) {
-  const uint32_t gw[4] = {g.x, g.y, g.z, g.w}, ow[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-  const float2 half2 = make_float2(0.5f, 0.5f);
-  uint32_t r[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const float2 z = __fmul2_rn(__bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&gw[e])), half2);
-    float2 t;
-    asm("tanh.approx.f32 %0, %1;" : "=f"(t.x) : "f"(z.x));
-    asm("tanh.approx.f32 %0, %1;" : "=f"(t.y) : "f"(z.y));
-    const float2 q = __fmul2_rn(__ffma2_rn(t, half2, half2),
-                                make_float2(__uint_as_float(ow[2 * e]), __uint_as_float(ow[2 * e + 1])));
-    const __nv_bfloat162 h2 = __floats2bfloat162_rn(q.x, q.y);
-    r[e] = *reinterpret_cast<const uint32_t*>(&h2);
-  }
-  return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
 // A load that stays where it is written: the compiler would else move it to
@@ -637,7 +622,7 @@ __device__ __noinline__ void linear_output_role(uint32_t o_smem, uint32_t tmem, 
           b[i] = lds16((get_a ^ 128) + (i0 + i) * 4096);
         }
 #pragma unroll
-        for (int i = 0; i < kB; ++i) a[i] = gate_pack_tanh(g[i0 + i], a[i], b[i]);
+        for (int i = 0; i < kB; ++i) a[i] = gate_pack(g[i0 + i], a[i], b[i]);
 #pragma unroll
         for (int i = 0; i < kB; ++i, p += 16 * rs)
           if (cr + 16 * (i0 + i) < Lt && 64 * h < cols) st_out(p, a[i]);

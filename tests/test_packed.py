@@ -994,3 +994,52 @@ def test_dense_bounds_that_go_back(cuda_device, cu):
         ref, mag = ref_dense(q, k, v, gate, [a, b])
         check(out[a:b], ref[a:b], attn_tol(ref, mag)[a:b])
     assert bool((out[untouched] == 7).all())
+
+
+# ------------------------------------------------------------------------------------ closed gates
+
+def closed(g, *shape):
+    """Gates from wide open to closed: sigmoids of 1 down to 2^-86."""
+    return (torch.rand(shape, generator=g, device="cuda") * 70 - 60).to(BF)
+
+
+# a sigmoid's exponent |gate| log2(e) < 87 is rounded to fp32 (87 2^-24 ln 2 < 2^-18) before an exponential and a
+# reciprocal of a few ulp
+GATE = 2.0 ** -17
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lens,H,d", [([1], 1, 64), ([130, 1, 300], 4, 128), ([200, 77], 3, 64), ([2500], 2, 128)])
+def test_linear_packed_closed_gates(cuda_device, lens, H, d):
+    """Positive q, k and v: no sum cancels, so every output has a relative bound, however small its gate."""
+    cu, T = starts(lens), sum(lens)
+    q, k, v = (x.abs() for x in linear_inputs(T, H, d, seed=T)[:3])
+    gate = closed(gen(T + 1), T, H, d)
+    lam = decays(H)
+    out = sala.linear_packed_prefill(q, k, v, gate, lam, i32(cu))
+    clean()
+    ref, mag, _, _ = ref_linear(q, k, v, gate, lam, cu, [None] * len(lens))
+    check(out, ref, (HALF + GATE) * ref.abs() + HALF * (1 + HALF) * mag + 1e-30)
+    # the first token of each sequence through the step: no products in bf16, d fp32 additions (2^-17 for d = 128)
+    first = torch.tensor([c for c, n in zip(cu, lens) if n], device="cuda")
+    pool = torch.zeros((len(first), H, d, d), device="cuda")
+    one = sala.linear_packed_step(q[first], k[first], v[first], gate[first], lam, pool)
+    clean()
+    check(one, ref[first], (HALF + 3 * GATE) * ref[first].abs() + 1e-30)
+
+
+@pytest.mark.gpu
+def test_dense_and_prefix_closed_gates(cuda_device):
+    T, Hq, Hkv, d = 300, 8, 2, 128
+    q, k, v, _ = dense_inputs(T, Hq, Hkv, d, seed=5)
+    v, gate = v.abs(), closed(gen(6), T, Hq, d)
+    out = sala.dense_prefill(q, k, v, gate, i32([0, T]))
+    clean()
+    ref, mag = ref_dense(q, k, v, gate, [0, T])
+    check(out, ref, attn_tol(ref, mag) + GATE * ref)
+    t = prefix_inputs(5, 300, 100, Hq, Hkv, d, 7, seed=2)
+    t["v"], t["pv"], t["vc"], t["gate"] = t["v"].abs(), t["pv"].abs(), t["vc"].abs(), gate[:5].contiguous()
+    ref, mag = ref_prefix(t["q"], t["k"], t["v"], t["gate"], t["pk"], t["pv"], t["kc"], t["vc"], t["lens"], t["slots"])
+    out = call_prefix(t)
+    clean()
+    check(out, ref, attn_tol(ref, mag) + GATE * ref)
