@@ -34,7 +34,8 @@
 // Isolation.  Rows past a sequence's end become 0 in K and V before anything is
 // multiplied (0 x NaN is NaN).  So do non-finite values of V before P V, whose
 // zeros above the diagonal would else hand them to earlier tokens; the epilogue
-// adds them to the rows that do see them.
+// makes the rows that do see them NaN, which is what q S gives for a column of
+// infinities of both signs.
 //
 // q, k, v, gate and out are 160 KB per tile and head (d = 128), 7000 cycles of
 // an SM at this card's copy rate, against 2560 cycles of tensor core.  What binds
@@ -600,7 +601,7 @@ __device__ __noinline__ void linear_output_role(uint32_t o_smem, uint32_t tmem, 
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             const float x = to_f32(vr[e]);
-            if (!isfinite(x)) o[e] += x;
+            if (!isfinite(x)) o[e] = NAN;
           }
         }
       }

@@ -379,7 +379,8 @@ size_t sala_linear_packed_workspace_size(const sala_packed_linear_desc* d);
  * states they end with, or NULL; it may be state_in.  Entries that no
  * sequence names are left as they are; a sequence of length 0 hands its state
  * on.  A padded sequence (negative slot) starts from zeros, and its tokens'
- * outputs are written. lambda in [0, 1]. */
+ * outputs are written.  lambda in [0, 1].  A value of v that is not finite
+ * makes its column of the outputs NaN from its token on. */
 sala_status sala_linear_packed_prefill(const sala_packed_linear_desc* d, const void* q_norm,
                                        const void* k_norm, const void* v, const void* gate,
                                        const float* lambda, const int32_t* cu_seqlens,

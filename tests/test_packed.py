@@ -1043,3 +1043,28 @@ def test_dense_and_prefix_closed_gates(cuda_device):
     out = call_prefix(t)
     clean()
     check(out, ref, attn_tol(ref, mag) + GATE * ref)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
+@pytest.mark.parametrize("d", [64, 128])
+def test_linear_packed_nonfinite_values_keep_no_sign(cuda_device, bad, d):
+    """An infinite value leaves infinities of both signs in its column of the state, and q times those is
+    NaN: the outputs that see it are NaN in its own tile, as in the tiles behind it and in the step."""
+    T, H, u = 300, 2, 40
+    q, k, v, gate = linear_inputs(T, H, d, seed=4)
+    lam = decays(H)
+    want = sala.linear_packed_prefill(q, k, v, gate, lam, i32([0, T]))
+    v[u, 1, 9] = bad
+    ref, _, S, _ = ref_linear(q, k, v, gate, lam, [0, T], [None])
+    assert bool(ref[u:, 1, 9].isnan().all())
+    got = sala.linear_packed_prefill(q, k, v, gate, lam, i32([0, T]))
+    clean()
+    assert bool(got[u:, 1, 9].isnan().all())
+    keep = torch.ones_like(want, dtype=torch.bool)
+    keep[u:, 1, 9] = False
+    assert torch.equal(got[keep], want[keep])
+    one = sala.linear_packed_step(*(x[u:u + 1].contiguous() for x in (q, k, v, gate)), lam,
+                                  torch.zeros((1, H, d, d), device="cuda"))
+    clean()
+    assert bool(one[0, 1, 9].isnan())
