@@ -322,8 +322,9 @@ sala_status sala_decode_step(const sala_decode_desc* d, const sala_decode_io* io
  *     slots [n] int32 names the entry of each sequence (row).  NULL: entry i
  *     for sequence i (n_slots >= n).  A negative slot marks a padded row,
  *     which is skipped: nothing of it is written.  A slot >= n_slots, or one
- *     that an earlier row of the call names too, is skipped likewise and sets
- *     the bounds bit.
+ *     that an earlier row of the call names too, is refused: the row is
+ *     skipped likewise and the bounds bit set.  (Prompts of the linear layer
+ *     have outputs all the same: see there.)
  *   - The calls read lengths and slots on the device only, so a call captured
  *     into a CUDA graph follows what these arrays hold at replay.  Two calls
  *     that may overlap on the GPU (captured graphs among them) need a
@@ -378,8 +379,9 @@ size_t sala_linear_packed_workspace_size(const sala_packed_linear_desc* d);
  * states the sequences start from, or NULL for zeros; state_out: pool of the
  * states they end with, or NULL; it may be state_in.  Entries that no
  * sequence names are left as they are; a sequence of length 0 hands its state
- * on.  A padded sequence (negative slot) starts from zeros, and its tokens'
- * outputs are written.  lambda in [0, 1].  A value of v that is not finite
+ * on.  A sequence whose slot is negative or refused starts from zeros, and its
+ * tokens' outputs are written, but no state of it is: after the bounds bit,
+ * discard them.  lambda in [0, 1].  A value of v that is not finite
  * makes its column of the outputs NaN from its token on. */
 sala_status sala_linear_packed_prefill(const sala_packed_linear_desc* d, const void* q_norm,
                                        const void* k_norm, const void* v, const void* gate,
