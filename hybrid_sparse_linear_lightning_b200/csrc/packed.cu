@@ -240,9 +240,20 @@ struct PrefixPlan {
   int Tt, pairs;                 // requests per row tile, pairs of row tiles
   int mtiles;                    // 16-row tiles of a group
   bool walked;                   // the prefix is read with each request's own keys
+  int cluster;                   // CTAs that share a request's keys
   int split_blocks, n_split;     // else: key blocks per part of the prefix, parts
   size_t o, ml, total;           // workspace: parts of O, of (maximum, sum)
 };
+
+// CTAs per cluster for `units` of up to `keys` keys each: clusters grow until
+// their CTAs fill the card twice over (two CTAs live on an SM), as long as every
+// warp has eight steps, and over SMs that would stay idle down to two steps.
+int own_cluster(int64_t units, int64_t keys) {
+  int cs = 1;
+  while (cs < kOwnMaxCluster && units * cs < 4 * 148 && keys > (int64_t)cs * kOwnWarps * 16 * 8) cs *= 2;
+  while (cs < kOwnMaxCluster && units * cs * 2 <= 148 && keys > (int64_t)cs * kOwnWarps * 16 * 2) cs *= 2;
+  return cs;
+}
 
 PrefixPlan prefix_plan(const sala_prefix_desc* d) {
   constexpr int kSms = 148;
@@ -252,7 +263,13 @@ PrefixPlan prefix_plan(const sala_prefix_desc* d) {
   p.pairs = (int)((tiles + 1) / 2);
   const int64_t blocks = ((int64_t)d->prefix_len + kPaBlock - 1) / kPaBlock;
   p.mtiles = (d->q_heads / d->kv_heads + 15) / 16;
-  p.walked = (double)d->batch * d->kv_heads * p.mtiles * d->prefix_len * d->head_dim * 4 <= 24e6;
+  // walked where that reads little and is short for each warp: packed_decode.cuh
+  // has both sides
+  const int64_t own_units = (int64_t)d->batch * d->kv_heads * p.mtiles;
+  p.cluster = own_cluster(own_units, d->cache_capacity + d->prefix_len);
+  p.walked = (double)own_units * d->prefix_len * d->head_dim * 4 <= 24e6 &&
+             d->prefix_len <= p.cluster * kOwnWarps * 16 * kOwnMaxWalk;
+  if (!p.walked) p.cluster = own_cluster(own_units, d->cache_capacity);
   if (blocks > 0 && !p.walked) {
     // the number of parts whose waves of units take the fewest block times; a
     // unit costs two blocks' time to start and to hand over its part
@@ -302,15 +319,8 @@ sala_status run_prefix(const sala_prefix_desc* d, const void* q, const void* k, 
     const sala_status s = launch_status();
     if (s != SALA_OK) return s;
   }
-  // clusters grow until their CTAs fill the card twice over (two CTAs live on an
-  // SM), as long as every warp has eight steps of a full cache
-  const int mtiles = p.mtiles, walked = p.walked ? d->prefix_len : 0;
+  const int mtiles = p.mtiles, walked = p.walked ? d->prefix_len : 0, cs = p.cluster;
   const int64_t units = (int64_t)d->batch * d->kv_heads * mtiles;
-  const int64_t keys = d->cache_capacity + walked;
-  int cs = 1;
-  while (cs < kOwnMaxCluster && units * cs < 4 * 148 && keys > (int64_t)cs * kOwnWarps * 16 * 8) cs *= 2;
-  // and over SMs that would stay idle down to two steps
-  while (cs < kOwnMaxCluster && units * cs * 2 <= 148 && keys > (int64_t)cs * kOwnWarps * 16 * 2) cs *= 2;
   if (units * cs > 0x7fffffffll) return SALA_ERR_UNSUPPORTED;
   auto kern = own_attn_kernel<D>;
   const size_t smem = OwnLayout<D>::kBytes;

@@ -11,10 +11,14 @@
 //      parts through distributed shared memory with those of the prefix, gates,
 //      and appends the token to the cache.
 //
-// A prefix that takes little to read once for every request (24 MB in all) is
-// walked by the second kernel with the own keys, and there is no first: 5 requests
-// over 700 tokens 5.5 us against 9.0, 16 over 1000 (16 MB) 9.4 against 11.4, 8 over
-// 4000 (33 MB) 14.8 against 14.7, 16 over 2000 of 8 kv heads (131 MB) 42 against 16.
+// A prefix that takes little to read once for every request (24 MB in all), and
+// that gives no warp more than 18 steps of 16 keys, is walked by the second kernel
+// with the own keys, and there is no first: 5 requests over 700 tokens 5.5 us against
+// 9.0, 16 over 1000 (16 MB) 9.4 against 11.4, 8 over 4000 (33 MB) 14.8 against 14.7,
+// 16 over 2000 of 8 kv heads (131 MB) 42 against 16.  Few requests have few clusters,
+// whose warps take 0.7 us a step: one request of 2 kv heads over 8000 tokens (16
+// steps) 17.7 us against 21.6, over 10000 (20) 20.4 against 17.9, over 20000 (39) 33
+// against 24; one kv head over 32768 (64) 49 against 25.
 //
 // The second launch starts while the first runs out (programmatic dependent
 // launch) and waits for it before it reads the prefix's parts.
@@ -43,6 +47,7 @@ constexpr int kOwnWarps = 4;
 constexpr int kOwnStages = 3;
 constexpr int kOwnMaxSplits = 64;      // parts of the prefix
 constexpr int kOwnMaxCluster = 8;
+constexpr int kOwnMaxWalk = 18;        // steps of a warp over a walked prefix
 
 template <int D>
 struct OwnLayout {

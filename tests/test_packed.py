@@ -1068,3 +1068,31 @@ def test_linear_packed_nonfinite_values_keep_no_sign(cuda_device, bad, d):
                                   torch.zeros((1, H, d, d), device="cuda"))
     clean()
     assert bool(one[0, 1, 9].isnan())
+
+
+# ------------------------------------------------------------------ which way a prefix is read
+
+def prefix_need(B, P, cap, Hq, Hkv, d, n_slots=None):
+    """Workspace of a prefix decode: none where the prefix is walked with the own keys."""
+    return sala.LIB.sala_prefix_workspace_size(ctypes.byref(prefix_desc(
+        batch=B, prefix_len=P, n_slots=n_slots or B, q_heads=Hq, kv_heads=Hkv, head_dim=d, cache_capacity=cap)))
+
+
+def test_a_long_prefix_of_few_requests_is_not_walked():
+    """One request has eight CTAs to walk a prefix with: long ones are shared out over the card instead."""
+    for Hq, Hkv, d in ((16, 1, 128), (32, 2, 128), (4, 1, 64)):
+        for B in (1, 2):
+            assert prefix_need(B, 32768, 256, Hq, Hkv, d) > 0
+            assert prefix_need(B, 20000, 256, Hq, Hkv, d) > 0
+            assert prefix_need(B, 8000, 256, Hq, Hkv, d) == 0
+    assert prefix_need(5, 700, 192, 4, 1, 64) == 0 and prefix_need(64, 32768, 1024, 32, 2, 128) > 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,P,cap,Hq,Hkv,d", [(1, 20000, 100, 16, 1, 128), (2, 9300, 700, 8, 2, 64), (1, 9200, 5, 7, 1, 128)])
+def test_prefix_decode_of_few_requests(cuda_device, B, P, cap, Hq, Hkv, d):
+    t = prefix_inputs(B, P, cap, Hq, Hkv, d, B + 2, seed=B + P)
+    ref, mag = ref_prefix(t["q"], t["k"], t["v"], t["gate"], t["pk"], t["pv"], t["kc"], t["vc"], t["lens"], t["slots"])
+    out = call_prefix(t)
+    clean()
+    check(out, ref, attn_tol(ref, mag))
