@@ -69,8 +69,8 @@ sala_status check_prefix(const sala_prefix_desc* d) {
     return SALA_ERR_INVALID_ARG;
   const sala_status s = check_heads(d->q_heads, d->kv_heads, d->head_dim);
   if (s != SALA_OK) return s;
-  // cache rows are addressed by 32-bit tile coordinates
-  if (d->cache_capacity * d->n_slots > 0x7fffffffll) return SALA_ERR_UNSUPPORTED;
+  // more cache rows than any card holds; keys are counted in 32 bits
+  if (d->cache_capacity > 0x7fffffffll / d->n_slots) return SALA_ERR_UNSUPPORTED;
   return d->dtype == SALA_BF16 ? SALA_OK : SALA_ERR_UNSUPPORTED;
 }
 

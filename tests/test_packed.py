@@ -1096,3 +1096,12 @@ def test_prefix_decode_of_few_requests(cuda_device, B, P, cap, Hq, Hkv, d):
     out = call_prefix(t)
     clean()
     check(out, ref, attn_tol(ref, mag))
+
+
+def test_a_cache_beyond_64_bits_is_refused():
+    for cap, n in ((1 << 62, 4), (1 << 61, 8), ((1 << 63) - 1, 2), (1 << 30, 4)):
+        d = prefix_desc(batch=2, prefix_len=32768, n_slots=n, cache_capacity=cap)
+        assert sala.LIB.sala_prefix_workspace_size(ctypes.byref(d)) == 0
+        assert raw("sala_prefix_decode", d, *[FAKE] * 9, None, FAKE, None, 0) == sala.SALA_ERR_UNSUPPORTED
+    d = prefix_desc(batch=2, prefix_len=32768, n_slots=2, cache_capacity=(1 << 30) - 1)
+    assert raw("sala_prefix_decode", d, *[FAKE] * 9, None, FAKE, None, 0) == sala.SALA_ERR_WORKSPACE
