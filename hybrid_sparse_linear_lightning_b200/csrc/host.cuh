@@ -20,6 +20,9 @@ inline size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 
 inline bool aligned16(const void* p) { return p && ((uintptr_t)p & 15u) == 0; }
 inline bool aligned16_or_null(const void* p) { return !p || ((uintptr_t)p & 15u) == 0; }
+// arrays that are read value by value: slices of them may start anywhere
+inline bool aligned4(const void* p) { return p && ((uintptr_t)p & 3u) == 0; }
+inline bool aligned4_or_null(const void* p) { return ((uintptr_t)p & 3u) == 0; }
 
 // kernels launched by this process (all devices, all entry points)
 inline std::atomic<uint64_t> g_launches{0};

@@ -357,7 +357,7 @@ sala_status sala_qk_norm(const sala_qk_norm_desc* d, const void* q, const void* 
   const sala_status s = check_qk_norm(d);
   if (s != SALA_OK) return s;
   if (!aligned16(q) || !aligned16(k) || !aligned16(wq) || !aligned16(wk) || !aligned16(q_norm) ||
-      !aligned16(k_norm) || !aligned16_or_null(positions))
+      !aligned16(k_norm) || !aligned4_or_null(positions))
     return SALA_ERR_INVALID_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (d->dtype == SALA_BF16) {
@@ -379,7 +379,7 @@ sala_status sala_dense_prefill(const sala_dense_desc* d, const void* q_norm, con
   const sala_status s = check_dense(d);
   if (s != SALA_OK) return s;
   if (!aligned16(q_norm) || !aligned16(k_norm) || !aligned16(v) || !aligned16(gate) ||
-      !aligned16(cu_seqlens) || !aligned16(out))
+      !aligned4(cu_seqlens) || !aligned16(out))
     return SALA_ERR_INVALID_ARG;
   (void)workspace;
   (void)ws_bytes;
@@ -404,7 +404,7 @@ sala_status sala_linear_packed_prefill(const sala_packed_linear_desc* d, const v
   if (s != SALA_OK) return s;
   if (d->dtype != SALA_BF16) return SALA_ERR_UNSUPPORTED;
   if (!aligned16(q_norm) || !aligned16(k_norm) || !aligned16(v) || !aligned16(gate) ||
-      !aligned16(lambda) || !aligned16(cu_seqlens) || !aligned16_or_null(slots) ||
+      !aligned4(lambda) || !aligned4(cu_seqlens) || !aligned4_or_null(slots) ||
       !aligned16_or_null(state_in) || !aligned16_or_null(state_out) || !aligned16(out))
     return SALA_ERR_INVALID_ARG;
   if (!slots && d->n_slots < d->n_seqs) return SALA_ERR_INVALID_ARG;
@@ -426,7 +426,7 @@ sala_status sala_linear_packed_step(const sala_packed_linear_desc* d, const void
   if (s != SALA_OK) return s;
   if (d->tokens != d->n_seqs) return SALA_ERR_INVALID_ARG;
   if (!aligned16(q_norm) || !aligned16(k_norm) || !aligned16(v) || !aligned16(gate) ||
-      !aligned16(lambda) || !aligned16_or_null(slots) || !aligned16(state) || !aligned16(out))
+      !aligned4(lambda) || !aligned4_or_null(slots) || !aligned16(state) || !aligned16(out))
     return SALA_ERR_INVALID_ARG;
   if (!slots && d->n_slots < d->n_seqs) return SALA_ERR_INVALID_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -451,7 +451,7 @@ sala_status sala_prefix_decode(const sala_prefix_desc* d, const void* q_norm, co
   const sala_status s = check_prefix(d);
   if (s != SALA_OK) return s;
   if (!aligned16(q_norm) || !aligned16(k_norm) || !aligned16(v) || !aligned16(gate) ||
-      !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(lens) || !aligned16_or_null(slots) ||
+      !aligned16(k_cache) || !aligned16(v_cache) || !aligned4(lens) || !aligned4_or_null(slots) ||
       !aligned16(out))
     return SALA_ERR_INVALID_ARG;
   if (d->prefix_len > 0 && (!aligned16(prefix_k) || !aligned16(prefix_v))) return SALA_ERR_INVALID_ARG;

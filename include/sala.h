@@ -329,6 +329,8 @@ sala_status sala_decode_step(const sala_decode_desc* d, const sala_decode_io* io
  *     into a CUDA graph follows what these arrays hold at replay.  Two calls
  *     that may overlap on the GPU (captured graphs among them) need a
  *     workspace each.
+ *   - cu_seqlens, slots, lens, positions and lambda need be 4-byte aligned only
+ *     (slices of longer arrays); everything else is 16-byte aligned.
  *   - q_norm and k_norm are bf16 whatever the dtype, as everywhere here. */
 
 /* QK-RMSNorm of packed tokens and, with positions, RoPE: what

@@ -1105,3 +1105,49 @@ def test_a_cache_beyond_64_bits_is_refused():
         assert raw("sala_prefix_decode", d, *[FAKE] * 9, None, FAKE, None, 0) == sala.SALA_ERR_UNSUPPORTED
     d = prefix_desc(batch=2, prefix_len=32768, n_slots=2, cache_capacity=(1 << 30) - 1)
     assert raw("sala_prefix_decode", d, *[FAKE] * 9, None, FAKE, None, 0) == sala.SALA_ERR_WORKSPACE
+
+
+# --------------------------------------------------------------- slices of per-request arrays
+
+def test_arrays_read_by_value_need_four_byte_alignment():
+    """A scheduler hands over slices: 4-byte alignment passes on to the next check (the workspace's)."""
+    by4, by2 = ctypes.c_void_p(0x10004), ctypes.c_void_p(0x10002)
+    d = lin_desc(tokens=9000, n_seqs=3, heads=32, head_dim=128)
+    call = lambda lam, cu, slots: raw("sala_linear_packed_prefill", d, *[FAKE] * 4, lam, cu, slots, None, None, FAKE,
+                                      None, 0)
+    assert call(by4, by4, by4) == sala.SALA_ERR_WORKSPACE
+    for at in range(3):
+        assert call(*[by2 if i == at else FAKE for i in range(3)]) == sala.SALA_ERR_INVALID_ARG
+    d2 = prefix_desc(prefix_len=32768)
+    call = lambda lens, slots: raw("sala_prefix_decode", d2, *[FAKE] * 8, lens, slots, FAKE, None, 0)
+    assert call(by4, by4) == sala.SALA_ERR_WORKSPACE
+    assert call(by2, FAKE) == call(FAKE, by2) == sala.SALA_ERR_INVALID_ARG
+    assert raw("sala_qk_norm", qk_desc(), *[FAKE] * 4, by2, FAKE, FAKE) == sala.SALA_ERR_INVALID_ARG
+    assert raw("sala_dense_prefill", dense_desc(), *[FAKE] * 4, by2, FAKE, FAKE, BIG) == sala.SALA_ERR_INVALID_ARG
+    assert raw("sala_linear_packed_step", lin_desc(), *[FAKE] * 4, by2, FAKE, FAKE, FAKE) == sala.SALA_ERR_INVALID_ARG
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("skip", [1, 2, 3])
+def test_slices_of_per_request_arrays(cuda_device, skip):
+    tail = lambda x: torch.cat([torch.full((skip,), 99, dtype=x.dtype, device="cuda"), x])[skip:]
+    g, cu = gen(3), i32([0, 70, 200, 201])
+    w = torch.ones(64, device="cuda")
+    q, k, v, gate = linear_inputs(201, 3, 64, seed=3)
+    pos = torch.arange(201, device="cuda").int()
+    for a, b in zip(sala.qk_norm(q, k, w, w, pos), sala.qk_norm(q, k, w, w, tail(pos))):
+        assert torch.equal(a, b)
+    assert torch.equal(sala.dense_prefill(q, k, v, gate, cu), sala.dense_prefill(q, k, v, gate, tail(cu)))
+    pool, lam, slots = torch.randn((5, 3, 64, 64), generator=g, device="cuda"), decays(3), i32([4, 0, 2])
+    one, two = pool.clone(), pool.clone()
+    a = sala.linear_packed_prefill(q, k, v, gate, lam, cu, slots=slots, state_in=one, state_out=one)
+    b = sala.linear_packed_prefill(q, k, v, gate, tail(lam), tail(cu), slots=tail(slots), state_in=two, state_out=two)
+    assert torch.equal(a, b) and torch.equal(one, two)
+    a = sala.linear_packed_step(q[:3], k[:3], v[:3], gate[:3], lam, one, slots=slots)
+    b = sala.linear_packed_step(q[:3], k[:3], v[:3], gate[:3], tail(lam), two, slots=tail(slots))
+    assert torch.equal(a, b) and torch.equal(one, two)
+    t = prefix_inputs(3, 500, 100, 8, 2, 64, 5, seed=4)
+    lens, slots = i32(t["lens"]), i32(t["slots"])
+    call = lambda n, s: sala.prefix_decode(t["q"], t["k"], t["v"], t["gate"], t["pk"], t["pv"], t["kc"], t["vc"], n, slots=s)
+    assert torch.equal(call(lens, slots), call(tail(lens), tail(slots)))
+    clean()
