@@ -9,12 +9,14 @@ import subprocess
 import sys
 import sysconfig
 from concurrent.futures import ThreadPoolExecutor
+from importlib.metadata import version
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libsala.so")
 CALLS = os.path.join(PKG, "_packed.so")           # Python module of the packed-batch calls, on libsala.so
+REPORT = os.path.join(PKG, "libsala.ptxas.json")
 CALLS_SOURCE = os.path.join(CSRC, "packed_calls.cpp")
 SOURCES = ["api.cu", "packed.cu"]
 
@@ -37,9 +39,17 @@ def nvcc_path() -> str:
     raise RuntimeError("nvcc not found")
 
 
+def built_for() -> dict:
+    """What the Python module depends on besides its sources: another one of these needs another build."""
+    return {"torch": version("torch"), "python": sysconfig.get_config_var("SOABI")}
+
+
 def needs_build() -> bool:
-    if not (os.path.exists(LIB) and os.path.exists(CALLS)):
+    if not (os.path.exists(LIB) and os.path.exists(CALLS) and os.path.exists(REPORT)):
         return True
+    with open(REPORT) as f:
+        if json.load(f).get("built_for") != built_for():
+            return True
     t = min(os.path.getmtime(LIB), os.path.getmtime(CALLS))
     deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(ROOT, "include", "sala.h")]
     return any(os.path.getmtime(p) > t for p in deps if os.path.isfile(p))
@@ -52,7 +62,6 @@ def needs_build() -> bool:
 REGISTER_SPLIT_KERNELS = {"linear_segout_kernel": 128}
 PACKED_SPLIT_KERNELS = {"dense_attn_kernel": 168, "prefix_attn_kernel": 168,
                         "linear_packed_kernel": 128}
-REPORT = os.path.join(PKG, "libsala.ptxas.json")
 
 
 def parse_ptxas(text: str) -> dict:
@@ -130,7 +139,7 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     check_register_splits(regs)
     check_register_splits(regs, PACKED_SPLIT_KERNELS)
     with open(REPORT, "w") as f:
-        json.dump({"registers_per_thread": regs}, f, indent=1, sort_keys=True)
+        json.dump({"registers_per_thread": regs, "built_for": built_for()}, f, indent=1, sort_keys=True)
     os.replace(LIB + ".tmp", LIB)
     os.replace(CALLS + ".tmp", CALLS)
     return LIB

@@ -159,8 +159,6 @@ def _load():
 
 LIB = _load()
 
-from . import _packed  # noqa: E402  (after libsala.so, which it is linked against)
-
 
 def status_string(s: int) -> str:
     return LIB.sala_status_string(int(s)).decode()
@@ -383,27 +381,44 @@ def sparse_prefill(q_norm, k_norm, v, gate, idx, *, block=64, topk=16, n_init=1,
 # stream unless one is given, take outputs and workspaces from torch's allocator where none are given,
 # and return the sala_status of a refused call.
 
-def _packed_call(fn, stream, *args):
+# The module is built against one torch and one Python, so it is imported at the first packed call: without
+# it the ctypes calls above still work.
+_packed = None
+
+
+def _load_packed():
+    global _packed
+    try:
+        from . import _packed as module
+    except ImportError as e:
+        raise ImportError(f"_packed.so (the packed-batch calls) is missing or built for another torch or Python: {e}; "
+                          "run `python -m hybrid_sparse_linear_lightning_b200.build`") from e
+    _packed = module
+    return module
+
+
+def _packed_call(name, stream, *args):
+    fn = getattr(_packed or _load_packed(), name)
     if stream is None:
         r = fn(*args)
     else:
         with torch.cuda.stream(stream):      # memory is reused in the order of the stream it was used on
             r = fn(*args)
     if type(r) is int:
-        raise SalaError(r, "sala_" + fn.__name__)
+        raise SalaError(r, "sala_" + name)
     return r
 
 
 def qk_norm(q, k, wq, wk, positions=None, *, rope_base=10000.0, rms_eps=1e-6, outs=None, stream=None):
     """QK-RMSNorm of packed tokens q [T, Hq, d], k [T, Hk, d]; RoPE at ``positions`` [T] int32 where
     given.  Returns (q_norm, k_norm), bf16."""
-    return _packed_call(_packed.qk_norm, stream, q, k, wq, wk, positions, rope_base, rms_eps, outs)
+    return _packed_call("qk_norm", stream, q, k, wq, wk, positions, rope_base, rms_eps, outs)
 
 
 def dense_prefill(q_norm, k_norm, v, gate, cu_seqlens, *, scale=0.0, out=None, ws=None, stream=None):
     """Causal attention over packed prompts: q_norm, gate [T, Hq, d], k_norm, v [T, Hkv, d] bf16,
     cu_seqlens [n + 1] int32.  Returns out [T, Hq, d]; rows of no sequence are not written."""
-    return _packed_call(_packed.dense_prefill, stream, q_norm, k_norm, v, gate, cu_seqlens, scale, out, ws)
+    return _packed_call("dense_prefill", stream, q_norm, k_norm, v, gate, cu_seqlens, scale, out, ws)
 
 
 def linear_packed_prefill(q_norm, k_norm, v, gate, lam, cu_seqlens, *, slots=None, state_in=None,
@@ -411,7 +426,7 @@ def linear_packed_prefill(q_norm, k_norm, v, gate, lam, cu_seqlens, *, slots=Non
     """Linear layer over packed prompts ([T, H, d] bf16); state pools [n_slots, H, d, d] fp32 (state_out
     may be state_in).  Without pools the slots (if any) index n entries.  Returns out; rows of no
     sequence are not written."""
-    return _packed_call(_packed.linear_packed_prefill, stream, q_norm, k_norm, v, gate, lam, cu_seqlens, slots,
+    return _packed_call("linear_packed_prefill", stream, q_norm, k_norm, v, gate, lam, cu_seqlens, slots,
                         state_in, state_out, scale, out, ws)
 
 
@@ -419,7 +434,7 @@ def linear_packed_step(q_norm, k_norm, v, gate, lam, state, *, slots=None, scale
                        stream=None):
     """One token of each request ([n, H, d]) through a linear layer; ``state`` [n_slots, H, d, d] fp32 is
     updated in place.  Returns out."""
-    return _packed_call(_packed.linear_packed_step, stream, q_norm, k_norm, v, gate, lam, state, slots, scale, out)
+    return _packed_call("linear_packed_step", stream, q_norm, k_norm, v, gate, lam, state, slots, scale, out)
 
 
 def prefix_decode(q_norm, k_norm, v, gate, prefix_k, prefix_v, k_cache, v_cache, lens, *, slots=None,
@@ -428,7 +443,7 @@ def prefix_decode(q_norm, k_norm, v, gate, prefix_k, prefix_v, k_cache, v_cache,
     v [B, Hkv, d], prefix_k, prefix_v [P, Hkv, d] (None for no prefix), k_cache, v_cache
     [n_slots, capacity, Hkv, d] bf16, lens [B] int32.  Appends the token to the caches (the caller
     advances ``lens``) and returns out [B, Hq, d]."""
-    return _packed_call(_packed.prefix_decode, stream, q_norm, k_norm, v, gate, prefix_k, prefix_v, k_cache, v_cache,
+    return _packed_call("prefix_decode", stream, q_norm, k_norm, v, gate, prefix_k, prefix_v, k_cache, v_cache,
                         lens, slots, scale, out, ws)
 
 

@@ -20,7 +20,11 @@ step: bf16 2^-8, relative):
     asked for, norm-wise 2^-20.
 """
 import ctypes
+import json
 import math
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -1151,3 +1155,38 @@ def test_slices_of_per_request_arrays(cuda_device, skip):
     call = lambda n, s: sala.prefix_decode(t["q"], t["k"], t["v"], t["gate"], t["pk"], t["pv"], t["kc"], t["vc"], n, slots=s)
     assert torch.equal(call(lens, slots), call(tail(lens), tail(slots)))
     clean()
+
+
+# ---------------------------------------------------------------------------- the Python module
+
+def test_the_older_calls_work_without_the_packed_module():
+    """_packed.so belongs to one torch and one Python; where it does not load, only the packed calls fail."""
+    code = ("import sys\n"
+            "sys.modules['hybrid_sparse_linear_lightning_b200._packed'] = None\n"
+            "import torch\n"
+            "from hybrid_sparse_linear_lightning_b200 import sala\n"
+            "assert sala.sala_version() >= 100 and sala.status_string(0)\n"
+            "x = torch.zeros((1, 1, 64), dtype=torch.bfloat16)\n"
+            "w = torch.ones(64)\n"
+            "try:\n"
+            "    sala.qk_norm(x, x, w, w)\n"
+            "except ImportError as e:\n"
+            "    assert 'build' in str(e)\n"
+            "else:\n"
+            "    raise SystemExit('the packed call ran')\n")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stdout + r.stderr
+
+
+def test_another_torch_or_python_needs_a_build(tmp_path, monkeypatch):
+    from hybrid_sparse_linear_lightning_b200 import build as B
+    for f in ("LIB", "CALLS", "REPORT"):
+        monkeypatch.setattr(B, f, str(tmp_path / f))
+    assert B.needs_build()
+    for f in ("LIB", "CALLS"):
+        (tmp_path / f).write_bytes(b"")
+    for what, want in ((B.built_for(), False), ({**B.built_for(), "torch": "0"}, True),
+                       ({**B.built_for(), "python": "x"}, True), (None, True)):
+        (tmp_path / "REPORT").write_text(json.dumps({"registers_per_thread": {}, "built_for": what}))
+        assert B.needs_build() is want, what
