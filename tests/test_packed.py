@@ -1190,3 +1190,108 @@ def test_another_torch_or_python_needs_a_build(tmp_path, monkeypatch):
                        ({**B.built_for(), "python": "x"}, True), (None, True)):
         (tmp_path / "REPORT").write_text(json.dumps({"registers_per_thread": {}, "built_for": what}))
         assert B.needs_build() is want, what
+
+
+# ------------------------------------------------- prefixes on both sides of the rule that walks them
+
+def test_workspaces_one_byte_short_are_refused():
+    for fn, size, d, n in (("sala_linear_packed_prefill", "sala_linear_packed_workspace_size",
+                            lin_desc(tokens=9000, n_seqs=3, heads=32, head_dim=128), 10),
+                           ("sala_prefix_decode", "sala_prefix_workspace_size", prefix_desc(prefix_len=32768), 11)):
+        need = getattr(sala.LIB, size)(ctypes.byref(d))
+        assert need > 0
+        assert raw(fn, d, *[FAKE] * n, FAKE, need - 1) == sala.SALA_ERR_WORKSPACE
+        assert raw(fn, d, *[FAKE] * n, None, need) == sala.SALA_ERR_WORKSPACE
+        assert raw(fn, d, *[FAKE] * n, MISALIGNED, need) == sala.SALA_ERR_INVALID_ARG
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,P,cap,Hq,Hkv,d", [
+    (9, 6000, 700, 16, 1, 128), (2, 3500, 64, 128, 1, 128), (6, 2500, 130, 100, 1, 64), (3, 9000, 100, 17, 1, 128),
+    (4, 5000, 33, 66, 2, 64), (1, 10001, 1, 5, 1, 64), (140, 513, 40, 8, 4, 128), (2, 9300, 2000, 128, 2, 128)])
+def test_prefix_decode_split(cuda_device, B, P, cap, Hq, Hkv, d):
+    """Parts of the prefix joined with the own keys' tiles of 16 heads, for groups of all sizes."""
+    assert prefix_need(B, P, cap, Hq, Hkv, d, B + 2) > 0
+    test_prefix_decode(cuda_device, B, P, cap, Hq, Hkv, d)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("P", [200, 9000])
+def test_prefix_decode_skipped_rows_both_ways(cuda_device, P):
+    """Padded, doubled and out-of-range rows leave early, where a second launch waits and where there is none."""
+    assert (prefix_need(6, P, 64, 4, 2, 64) > 0) == (P == 9000)
+    t = prefix_inputs(6, P, 64, 4, 2, 64, 6, seed=3)
+    t["slots"] = [5, -1, 5, 9, 2, 0]
+    t["lens"] = [10, 3, 4, 5, 64, 63]
+    kc0, vc0 = t["kc"].clone(), t["vc"].clone()
+    ref, mag = ref_prefix(t["q"], t["k"], t["v"], t["gate"], t["pk"], t["pv"], kc0, vc0, t["lens"],
+                          [5, -1, -1, -1, -1, 0])
+    kc0[5, 10], kc0[0, 63] = t["k"][0], t["k"][5]
+    vc0[5, 10], vc0[0, 63] = t["v"][0], t["v"][5]
+    for _ in range(3):           # calls one behind the other: an early exit must not let the next one in
+        out = torch.full((6, 4, 64), 7.0, dtype=BF, device="cuda")
+        call_prefix(t, out=out)
+        torch.cuda.synchronize()
+        assert sala.sala_get_device_status() == sala.SALA_ERR_DEVICE_FAULT
+        for b in (0, 5):
+            check(out[b], ref[b], attn_tol(ref, mag)[b])
+        assert bool((out[1:5] == 7).all())
+        assert torch.equal(t["kc"], kc0) and torch.equal(t["vc"], vc0)
+    t["slots"] = [-1] * 6
+    out = torch.full((6, 4, 64), 7.0, dtype=BF, device="cuda")
+    call_prefix(t, out=out)
+    clean()
+    assert bool((out == 7).all()) and torch.equal(t["kc"], kc0) and torch.equal(t["vc"], vc0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("P", [300, 6000])
+def test_prefix_decode_isolation_both_ways(cuda_device, P):
+    assert (prefix_need(4, P, 200, 8, 2, 128) > 0) == (P == 6000)
+    t = prefix_inputs(4, P, 200, 8, 2, 128, 4, seed=3)
+    t["lens"] = [150, 199, 20, 130]
+    want = call_prefix(t)
+    s = t["slots"][1]
+    t["kc"][s, 7, 0, 3] = math.nan
+    t["vc"][s, 9, 1, 4] = math.inf
+    t["q"][2, 5] = math.inf
+    t["gate"][3, 1, 6] = math.nan
+    got = call_prefix(t)
+    clean()
+    ok = torch.ones_like(want, dtype=torch.bool)
+    ok[1, :4] = False
+    ok[1, 4:, 4] = False
+    ok[2, 5] = False
+    ok[3, 1, 6] = False
+    assert torch.equal(got[ok], want[ok])
+    assert bool(got[1, :4].isnan().all()) and bool(got[2, 5].isnan().all()) and not bool(got[1, 4:, 4].isfinite().any())
+    assert bool(got[3, 1, 6].isnan())
+    # the prefix is everyone's: a bad key there reaches the rows of its kv head, and no others
+    t["q"][2, 5] = 1.0
+    t["pk"][P // 2, 1, 0] = math.nan
+    got = call_prefix(t)
+    clean()
+    assert bool(got[:, 4:].isnan().all())
+    assert torch.equal(got[0, :4], want[0, :4]) and torch.equal(got[2, :4], want[2, :4])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("P", [300, 9500])
+def test_prefix_decode_on_streams_both_ways(cuda_device, P):
+    """Two calls on two streams at once, a workspace each; without slots."""
+    assert (prefix_need(5, P, 100, 8, 2, 64, 7) > 0) == (P == 9500)
+    runs = []
+    for seed in (2, 3):
+        t = prefix_inputs(5, P, 100, 8, 2, 64, 7, seed=seed)
+        t["slots"] = list(range(5))
+        ref = ref_prefix(t["q"], t["k"], t["v"], t["gate"], t["pk"], t["pv"], t["kc"], t["vc"], t["lens"], t["slots"])
+        runs.append((t, i32(t["lens"]), ref, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    outs = [[sala.prefix_decode(t["q"], t["k"], t["v"], t["gate"], t["pk"], t["pv"], t["kc"], t["vc"], lens, stream=s)
+             for t, lens, _, s in runs] for _ in range(4)]
+    torch.cuda.synchronize()
+    for row in outs:
+        for out, first, (_, _, (ref, mag), _) in zip(row, outs[0], runs):
+            check(out, ref, attn_tol(ref, mag))
+            assert torch.equal(out, first)
+    clean()
