@@ -102,6 +102,19 @@ struct Workspace {
   }
 };
 
+// Two objects of a list or tuple, or None twice for None.
+struct Pair {
+  PyObject* seq = nullptr;
+  Pair(PyObject* o, const char* name) {
+    if (o == Py_None) return;
+    if ((!PyList_Check(o) && !PyTuple_Check(o)) || PySequence_Fast_GET_SIZE(o) != 2)
+      refuse(std::string(name) + ": expected a pair of tensors");
+    seq = o;
+  }
+  PyObject* first() const { return seq ? PySequence_Fast_GET_ITEM(seq, 0) : Py_None; }
+  PyObject* second() const { return seq ? PySequence_Fast_GET_ITEM(seq, 1) : Py_None; }
+};
+
 sala_dtype dtype_code(const char* name, const Tensor& t) {
   if (t.scalar_type() == at::kBFloat16) return SALA_BF16;
   if (t.scalar_type() == at::kFloat) return SALA_F32;
@@ -131,11 +144,10 @@ PyObject* qk_norm(PyObject* const* a) {
   const Tensor& wq = expect("wq", a[2], {D}, F32, dev);
   const Tensor& wk = expect("wk", a[3], {D}, F32, dev);
   const Tensor pos = optional("positions", a[4], {T}, I32, dev);
+  const Pair outs(a[7], "outs");
   on_cuda("sala_qk_norm", dev);
   const c10::cuda::CUDAGuard guard(dev);
-  PyObject *oq = Py_None, *ok = Py_None;
-  if (a[7] != Py_None && !PyArg_ParseTuple(a[7], "OO;outs: a pair of tensors", &oq, &ok)) throw Refused{};
-  Tensor qn = output("q_norm", oq, {T, Hq, D}, BF, dev), kn = output("k_norm", ok, {T, Hk, D}, BF, dev);
+  Tensor qn = output("q_norm", outs.first(), {T, Hq, D}, BF, dev), kn = output("k_norm", outs.second(), {T, Hk, D}, BF, dev);
   const sala_qk_norm_desc d = {count(T, "tokens"), count(Hq, "heads"), count(Hk, "heads"), count(D, "head_dim"),
                                dtype_code("q", q), number(a[5]), number(a[6])};
   const sala_status s = sala_qk_norm(&d, ptr(q), ptr(k), (const float*)ptr(wq), (const float*)ptr(wk),

@@ -1295,3 +1295,28 @@ def test_prefix_decode_on_streams_both_ways(cuda_device, P):
             check(out, ref, attn_tol(ref, mag))
             assert torch.equal(out, first)
     clean()
+
+
+# ------------------------------------------------------------------------------ helper arguments
+
+def test_outs_may_be_any_pair():
+    x, w = torch.zeros((2, 1, 64), dtype=BF), torch.ones(64)
+    for outs in ([x, x.clone()], (x, x.clone())):         # gets as far as the device
+        with pytest.raises(ValueError, match="CUDA device"):
+            sala.qk_norm(x, x, w, w, outs=outs)
+    for outs in ([x], (x, x, x), x, 5):
+        with pytest.raises((TypeError, ValueError), match="outs"):
+            sala.qk_norm(x, x, w, w, outs=outs)
+
+
+@pytest.mark.gpu
+def test_qk_norm_outs_in_a_list(cuda_device):
+    g = gen(3)
+    q, k, w = rnd(g, 5, 4, 64), rnd(g, 5, 2, 64), torch.ones(64, device="cuda")
+    want = sala.qk_norm(q, k, w, w)
+    outs = [torch.empty_like(q), torch.empty_like(k)]
+    assert sala.qk_norm(q, k, w, w, outs=outs) is outs
+    with pytest.raises(ValueError, match="outs"):
+        sala.qk_norm(q, k, w, w, outs=[q])
+    clean()
+    assert torch.equal(outs[0], want[0]) and torch.equal(outs[1], want[1])
