@@ -402,6 +402,9 @@ def _packed_call(name, stream, *args):
     if stream is None:
         r = fn(*args)
     else:
+        device = getattr(args[0], "device", None)
+        if device is not None and stream.device != device:
+            raise ValueError(f"stream: on {stream.device}, the tensors are on {device}")
         with torch.cuda.stream(stream):      # memory is reused in the order of the stream it was used on
             r = fn(*args)
     if type(r) is int:

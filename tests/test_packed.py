@@ -1320,3 +1320,15 @@ def test_qk_norm_outs_in_a_list(cuda_device):
         sala.qk_norm(q, k, w, w, outs=[q])
     clean()
     assert torch.equal(outs[0], want[0]) and torch.equal(outs[1], want[1])
+
+
+def test_a_stream_of_another_device_is_refused():
+    """The call runs on the tensors' device; a stream of another one would be ignored there."""
+    class Stream:
+        device = torch.device("cuda:1")
+    z = lambda *s, dt=BF: torch.zeros(s, dtype=dt)
+    cu = torch.tensor([0, 4], dtype=torch.int32)
+    with pytest.raises(ValueError, match="stream"):
+        sala.dense_prefill(z(4, 2, 64), z(4, 1, 64), z(4, 1, 64), z(4, 2, 64), cu, stream=Stream())
+    with pytest.raises(ValueError, match="stream"):
+        sala.qk_norm(z(4, 2, 64), z(4, 1, 64), torch.ones(64), torch.ones(64), stream=Stream())
