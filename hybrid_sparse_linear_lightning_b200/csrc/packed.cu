@@ -177,7 +177,14 @@ LinearPlan linear_plan(const sala_packed_linear_desc* d) {
   } else {
     seg = tiles / 64;
   }
-  seg = std::min<int64_t>(std::max<int64_t>(seg, 8), 1 << 20);
+  // Down to two tiles, where there are 8 in all and a sequence has one on average:
+  // prompts of 1024, 3000 and 8192 tokens at 4 heads of 64 37 us, 38 and 39 against
+  // 72, 84 and 84 with 8 tiles, at 32 heads of 128 37, 70 and 158 against 63, 81 and
+  // 158.  Shorter calls are left whole, as the two launches more take longer (600
+  // tokens in 4 prompts, 32 heads of 128: 30 us, 45 cut at two), and so are many
+  // short prompts (20 of 1500 tokens, 8 heads of 128: 37 against 46).
+  const bool whole = per_head < 8 || d->tokens < (int64_t)kPlTile * d->n_seqs;
+  seg = std::min<int64_t>(std::max<int64_t>(seg, whole ? 8 : 2), 1 << 20);
   p.seg_tokens = (int)(seg * kPlTile);
   p.extra = d->tokens / p.seg_tokens;
   p.multi = std::min<int64_t>(p.extra, d->n_seqs);

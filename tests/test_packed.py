@@ -937,7 +937,7 @@ def usable(cu, T):
     return good
 
 
-# 2500 tokens: two heads of 128 are cut into segments of 1024, three for a whole sequence
+# 2500 tokens of two heads of 128 are cut into segments
 BACK = [[0, 2500, 0, 2500], [0, 2500, 0, 2500, 0, 2500], [0, 1100, 500, 2500], [2000, 1000, 1000, 2500],
         [0, 9999, 40, 2500], [7, 7, 3, 1200, 1200], list(range(0, 1201, 30)) + [600, 1500, 2500, 100, 200]]
 
@@ -1332,3 +1332,11 @@ def test_a_stream_of_another_device_is_refused():
         sala.dense_prefill(z(4, 2, 64), z(4, 1, 64), z(4, 1, 64), z(4, 2, 64), cu, stream=Stream())
     with pytest.raises(ValueError, match="stream"):
         sala.qk_norm(z(4, 2, 64), z(4, 1, 64), torch.ones(64), torch.ones(64), stream=Stream())
+
+
+def test_what_is_cut_into_segments():
+    need = lambda **kw: sala.LIB.sala_linear_packed_workspace_size(ctypes.byref(lin_desc(**{"n_slots": 64, **kw})))
+    for heads, d in ((4, 64), (8, 128), (32, 128)):
+        assert need(tokens=1024, n_seqs=1, heads=heads, head_dim=d) > 0
+        assert need(tokens=896, n_seqs=1, heads=heads, head_dim=d) == 0        # less than eight tiles
+        assert need(tokens=1023, n_seqs=8, heads=heads, head_dim=d) == 0       # less than a tile for each
