@@ -160,7 +160,7 @@ LinearPlan linear_plan(const sala_packed_linear_desc* d) {
   // one sequence and three tiles' time for what a segment costs besides.  With
   // sequences enough to fill the card twice, only what one SM would take more than
   // twice the whole card's time for is cut: the sums of the segments read keys and
-  // values once more (13 prompts of up to 23 tiles at 32 heads: 191 us whole, 198
+  // values once more (13 prompts of up to 23 tiles at 32 heads: 190 us whole, 197
   // cut at 17).
   const int64_t per_head = ((int64_t)d->tokens + kPlTile - 1) / kPlTile;
   int64_t seg = per_head;

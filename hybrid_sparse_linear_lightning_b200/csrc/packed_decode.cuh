@@ -25,7 +25,10 @@
 //
 // The own part is bound by memory: every key and value is used by one request
 // alone, 4 d bytes each, against 16 padded rows on warp-level matrix
-// instructions (m16n8k16).  Each warp keeps kOwnStages steps of 16 keys in
+// instructions (m16n8k16).  A group of more than 16 q heads reads them once per 16:
+// 12 requests with up to 16383 tokens of their own, 8 kv heads of 128, in 82 us for
+// groups of 16, 118 of 17, 124 of 32, 210 of 64 and 376 of 128 (the rereads hit L2
+// in part: 4.2 TB/s of keys asked for at 16, 7.2 at 128).  Each warp keeps kOwnStages steps of 16 keys in
 // flight with asynchronous copies of its own, so warps never wait for one
 // another before the final join.
 //

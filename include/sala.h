@@ -331,6 +331,8 @@ sala_status sala_decode_step(const sala_decode_desc* d, const sala_decode_io* io
  *     workspace each.
  *   - cu_seqlens, slots, lens, positions and lambda need be 4-byte aligned only
  *     (slices of longer arrays); everything else is 16-byte aligned.
+ *   - Outputs and the workspace overlap no input, but for the in-place uses
+ *     named at a call.
  *   - q_norm and k_norm are bf16 whatever the dtype, as everywhere here. */
 
 /* QK-RMSNorm of packed tokens and, with positions, RoPE: what
@@ -351,7 +353,8 @@ sala_status sala_qk_norm(const sala_qk_norm_desc* d, const void* q, const void* 
 
 /* The sparse layer's dense form: every query attends to all keys of its
  * sequence up to itself (what the block selection comes to for prompts that
- * fit into the selected blocks).  q_heads / kv_heads up to 128; SALA_BF16. */
+ * fit into the selected blocks; longer ones are attended to in full all the
+ * same, which is not what sala_sparse_prefill computes for them).  q_heads / kv_heads up to 128; SALA_BF16. */
 typedef struct {
   int tokens, n_seqs, q_heads, kv_heads, head_dim;
   sala_dtype dtype;
